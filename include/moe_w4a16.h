@@ -191,7 +191,7 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_forward_host_async(moe_w4a16_handle* h,
 MOE_W4A16_API moe_w4a16_status moe_w4a16_get_status(moe_w4a16_handle* h, int64_t* miss_count);
 
 /* Message of the last error on this handle ("" if none).  With h == NULL,
- * the message of the last failed create. */
+ * the message of the last failed create (or call without a handle). */
 MOE_W4A16_API const char* moe_w4a16_last_error(const moe_w4a16_handle* h);
 
 /* Limits of moe_w4a16_route_noalloc (its scratch is a fixed 5 MiB device array). */
@@ -427,6 +427,133 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_create_sim(int32_t num_experts, i
                                                           moe_w4a16_cache** out);
 MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_sim_complete(moe_w4a16_cache* c, uint64_t lease);
 MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_sim_fail(moe_w4a16_cache* c, int32_t where);
+
+/* ======================================================================
+ * Block operators: what an MoE block needs around its routed experts.
+ *
+ *   moe_w4a16_add_rmsnorm   residual addition + root-mean-square norm, with
+ *                           an optional 8-bit copy of the result
+ *   moe_w4a16_linear        dense matrix product with scales, bias,
+ *                           activation and residual in its epilogue (the
+ *                           router's logits, a shared expert)
+ *   moe_w4a16_route_scored  expert ids and weights from router logits:
+ *                           softmax or sigmoid scores, a balancing bias,
+ *                           groups, top-k, renormalised weights
+ *
+ * They need no handle, allocate nothing and keep nothing between calls.
+ * Work is enqueued on `stream` (the calling thread's current device); calls
+ * on different streams are independent, and every call may be captured in a
+ * CUDA graph.  All pointers are device memory.  Argument errors are returned
+ * synchronously with a message in moe_w4a16_last_error(NULL), and nothing is
+ * enqueued.  A row stride ("ld") counts elements; 0 means the row length.
+ * T == 0 enqueues nothing and returns OK.  Sums, norms and softmax
+ * statistics are FP32 (or wider); every output is rounded once, to nearest
+ * even.  An output may be the same tensor as an input only where said.
+ * ==================================================================== */
+
+/* element types */
+enum { MOE_W4A16_F16 = 0, MOE_W4A16_BF16 = 1, MOE_W4A16_F32 = 2, MOE_W4A16_E4M3 = 3 };
+
+typedef struct {
+  int32_t dtype;        /* F16 or BF16: x, residual, weight, residual_out, y */
+  int32_t hidden;       /* H: 1..16384 */
+  float eps;            /* >= 0 */
+  int32_t reserved;     /* 0 */
+  int64_t ld_x, ld_residual, ld_residual_out, ld_y, ld_q;
+} moe_w4a16_rmsnorm_config;
+
+/* Per row t (FP32):
+ *   s = x[t] + residual[t]                      (residual NULL: s = x[t])
+ *   n = s / sqrt(mean_h s^2 + eps) * weight     (weight NULL: 1)
+ *   residual_out[t] = s, y[t] = n               (each rounded to dtype; NULL to skip)
+ *   q_scale[t] = max_h |n| / 448
+ *   q[t] = n / q_scale[t] in E4M3, saturating   (q and q_scale: both or neither)
+ * The norm is taken of the unrounded sum and q of the unrounded n.  A row
+ * whose q_scale would fall below 2^-126 gets q_scale = 0 and q = 0.  NaN and
+ * infinities propagate within their row.  residual_out may be x or residual
+ * and y may be x (the same pointer and stride).  At least one output is
+ * required. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_add_rmsnorm(const moe_w4a16_rmsnorm_config* cfg, int64_t T, const void* x,
+                                                     const void* residual, const void* weight, void* residual_out,
+                                                     void* y, void* q, float* q_scale, moe_w4a16_stream_t stream);
+
+/* scores */
+enum { MOE_W4A16_SOFTMAX = 0, MOE_W4A16_SIGMOID = 1 };
+
+typedef struct {
+  int32_t dtype;        /* of the logits: F32, F16 or BF16 */
+  int32_t num_experts;  /* E: 1..512 */
+  int32_t top_k;        /* k: 1..32, <= top_groups * E / num_groups */
+  int32_t score;        /* SOFTMAX (over all E) or SIGMOID */
+  int32_t num_groups;   /* G: 1..32, divides E; experts e*G/E form group g */
+  int32_t top_groups;   /* 1..G groups stay eligible */
+  int32_t group_rank;   /* 1 or 2: a group is ranked by the sum of its 1 or 2 largest choices */
+  int32_t renormalize;  /* nonzero: the k weights are divided by their sum */
+  float scale;          /* finite; the weights are multiplied by it, last */
+  int32_t reserved;     /* 0 */
+  int64_t ld_logits;
+} moe_w4a16_route_config;
+
+/* Per row t of logits [T][E]:
+ *   score  = softmax or sigmoid of the logits
+ *   choice = score + bias                        (bias [E] FP32 or NULL: choice = score)
+ *   groups: only the experts of the top_groups groups with the largest group
+ *           values stay eligible (ties: lower group)
+ *   topk_ids [t][k] = the k largest choices, largest first (ties: lower
+ *           expert index);  topk_w = score[topk_ids] (/ their sum) * scale
+ * The bias decides the selection only; the weights come from the scores.
+ * The ids are those that 64-bit arithmetic gives: where two choices (or two
+ * groups) lie closer than the error of the FP32 scores, the row is redone in
+ * FP64.  A logit of -inf or NaN masks its expert: no score, never eligible; a
+ * bias of -inf or NaN takes the expert out of the selection, not out of the
+ * softmax.  A group's value counts its eligible choices (one, if it has only
+ * one); a group without any is last.  A row with fewer than k eligible
+ * experts fills up with the lowest unchosen indices at weight 0, so ids are
+ * always distinct and in [0, E). */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_route_scored(const moe_w4a16_route_config* cfg, int64_t T,
+                                                      const void* logits, const float* bias, int32_t* topk_ids,
+                                                      float* topk_w, moe_w4a16_stream_t stream);
+
+/* activations */
+enum {
+  MOE_W4A16_ACT_NONE = 0,
+  MOE_W4A16_ACT_RELU = 1,
+  MOE_W4A16_ACT_GELU = 2,        /* a/2 (1 + erf(a / sqrt 2)) */
+  MOE_W4A16_ACT_GELU_TANH = 3,   /* a/2 (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) */
+  MOE_W4A16_ACT_SILU = 4,        /* a / (1 + exp(-a)) */
+  MOE_W4A16_ACT_SWIGLU = 5       /* silu(gate) * up; W, w_scale and bias hold the N gate rows, then the N up rows */
+};
+
+typedef struct {
+  int32_t in_dtype;     /* x and W: F16, BF16 or E4M3 */
+  int32_t out_dtype;    /* out and residual: F16, BF16 or F32 */
+  int32_t n;            /* N: output features, >= 1 */
+  int32_t k;            /* K: input features, >= 1 */
+  int32_t act;          /* MOE_W4A16_ACT_* */
+  int32_t reserved;     /* 0 */
+  int64_t ld_x, ld_w, ld_residual, ld_out;
+} moe_w4a16_linear_config;
+
+/* out[t][n] = act(x_scale[t] * w_scale[m] * sum_k x[t][k] W[m][k] + bias[m]) + residual[t][n]
+ * with m = n, or for SWIGLU the gate m = n and the up m = N + n.
+ * W is [N][K] (SWIGLU: [2N][K]), K contiguous.  x_scale [T] and w_scale
+ * FP32, required for E4M3 and not allowed otherwise; bias FP32 or NULL;
+ * residual [T][N] in out_dtype or NULL, may be out itself (same stride).
+ * x and W must be 16-byte aligned with row strides of a multiple of 16 bytes
+ * (N, K and T may be odd).  Products accumulate in FP32 on the tensor cores;
+ * with few tokens K is split over the CTAs of a cluster and the parts are
+ * added in a fixed order, so a call's result does not change from run to
+ * run.  A bounded device wait that gave up is reported by
+ * moe_w4a16_block_status. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linear_config* cfg, int64_t T, const void* x,
+                                                const void* w, const float* x_scale, const float* w_scale,
+                                                const float* bias, const void* residual, void* out,
+                                                moe_w4a16_stream_t stream);
+
+/* Synchronises the calling thread's current device, reads and clears the
+ * status word of the block operators there: OK, or ERR_TIMEOUT if a bounded
+ * wait of moe_w4a16_linear gave up since the last call. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_block_status(void);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,48 @@
+// Declarations shared by the block operators (norm.cu, score.cu, linear.cu):
+// element types, conversions and argument errors.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <stdio.h>
+
+#include "moe_w4a16.h"
+#include "internal.h"
+
+namespace blk {
+
+DEV_INLINE float to_float(__half v) { return __half2float(v); }
+DEV_INLINE float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+DEV_INLINE float to_float(float v) { return v; }
+template <typename E>
+DEV_INLINE E from_float(float v);
+template <>
+DEV_INLINE __half from_float<__half>(float v) { return __float2half_rn(v); }
+template <>
+DEV_INLINE __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+DEV_INLINE float from_float<float>(float v) { return v; }
+
+// W neighbouring elements, loaded and stored at once.
+template <typename E, int W>
+struct alignas(sizeof(E) * W) Pack {
+  E v[W];
+};
+
+inline moe_w4a16_status reject(const char* op, const char* msg) {
+  char buf[256];
+  snprintf(buf, sizeof buf, "%s: %s", op, msg);
+  set_handle_free_error(buf);
+  return MOE_W4A16_ERR_INVALID_ARG;
+}
+
+inline moe_w4a16_status launch_failed(const char* op, cudaError_t e) {
+  cudaGetLastError();
+  char buf[256];
+  snprintf(buf, sizeof buf, "%s: %s", op, cudaGetErrorString(e));
+  set_handle_free_error(buf);
+  return MOE_W4A16_ERR_CUDA;
+}
+
+inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace blk

@@ -6,9 +6,9 @@
 
 The definitions, limits and masking rules are those of moe_w4a16_add_rmsnorm,
 moe_w4a16_linear and moe_w4a16_route_scored in include/moe_w4a16.h; this
-module checks tensors and marshals pointers.  Inputs are CUDA tensors of one
-device; a wrong shape, type or layout raises ValueError, an error of the
-library MoEError.  Rows may be strided (the last dimension contiguous).
+module and the compiled _block beside it check tensors and marshal pointers.
+Inputs are CUDA tensors of one device; a wrong shape, type or layout raises
+ValueError, an error of the library MoEError.  Rows may be strided (the last dimension contiguous).
 Outputs are allocated unless given; with stream=None work goes to the
 current stream.
 """
@@ -16,12 +16,13 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
+import os
 
 import torch
 
 from . import moe_w4a16 as _m
 
-_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5}
 _F32, _I32, _E4M3 = torch.float32, torch.int32, torch.float8_e4m3fn
@@ -58,22 +59,21 @@ def _lib():
     return lib
 
 
-# A config is plain numbers (shapes, types, strides): kept once per combination.
-@functools.lru_cache(maxsize=4096)
-def _config(cls, *fields):
-    cfg = cls(*fields)
-    return cfg, ctypes.addressof(cfg)
+_native = None   # the compiled module _block
 
 
-def _call(fn, stream, device, *args):
-    """fn(*args, stream) with `device` current."""
-    if device != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            st = fn(*args, _m._stream(stream))
-    else:
-        st = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream)
-    if st != _m.OK:
-        raise _m.MoEError(st, _lib().moe_w4a16_last_error(None).decode())
+def _load():
+    global _native
+    _lib()
+    path = os.path.join(os.path.dirname(_m.LIB_PATH), "_block.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"binding not built: {path} (run __graft_entry__.build())")
+    spec = importlib.util.spec_from_file_location("_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.set_error(_m.MoEError)
+    _native = mod
+    return mod
 
 
 def _empty(shape, dtype, like, stream):
@@ -84,35 +84,6 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _rows(name, t, T, n, dtype, device):
-    """Checks a [T, n] tensor with contiguous rows; returns (pointer, row stride)."""
-    if t.dtype != dtype or t.get_device() != device or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D {dtype} tensor on the device of the other arguments")
-    if t.shape[0] != T or t.shape[1] != n:
-        raise ValueError(f"{name} must have shape ({T}, {n}), got {tuple(t.shape)}")
-    ld, inner = t.stride()
-    if (inner != 1 and n > 1) or (ld < n and T > 1):
-        raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), ld if ld >= n else n
-
-
-def _vector(name, t, n, dtype, device):
-    if t.dtype != dtype or t.get_device() != device or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} on the device of the other arguments")
-    return t.data_ptr()
-
-
-def _input(name, x, dtypes):
-    if x.dtype not in dtypes or x.dim() != 2 or not x.is_cuda:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
-    return x.get_device()
-
-
-_NORM_TYPES = (torch.float16, torch.bfloat16)
-_LOGIT_TYPES = (torch.float32, torch.float16, torch.bfloat16)
-_LINEAR_TYPES = (torch.float16, torch.bfloat16, torch.float8_e4m3fn)
-
-
 def add_rmsnorm(x, residual=None, weight=None, *, eps: float = 1e-6, norm: bool = True, quant: bool = False, out=None,
                 stream=None):
     """s = x + residual, n = s / sqrt(mean s^2 + eps) * weight, per row of x [T, H] (fp16 or bf16).
@@ -121,32 +92,17 @@ def add_rmsnorm(x, residual=None, weight=None, *, eps: float = 1e-6, norm: bool 
     x's type (None without a residual), q = n / q_scale in E4M3 with one FP32
     scale per row (both None unless quant).  out: the same four, to be
     written (None where not returned); s may be x or residual, y may be x."""
-    dev = _input("x", x, _NORM_TYPES)
-    T, H = x.shape
-    dt = x.dtype
-    px, ldx = _rows("x", x, T, H, dt, dev)
-    pr = ldr = pso = ldso = py = ldy = pq = ldq = pqs = pw = 0
     if out is None:
-        y = _empty((T, H), dt, x, stream) if norm else None
-        s = _empty((T, H), dt, x, stream) if residual is not None else None
-        q = _empty((T, H), _E4M3, x, stream) if quant else None
-        qs = _empty((T,), _F32, x, stream) if quant else None
+        dt = x.dtype
+        y = _empty(x.shape, dt, x, stream) if norm else None
+        s = _empty(x.shape, dt, x, stream) if residual is not None else None
+        q = _empty(x.shape, _E4M3, x, stream) if quant else None
+        qs = _empty(x.shape[:1], _F32, x, stream) if quant else None
     else:
         y, s, q, qs = out
         if (y is None) == norm or (s is None) != (residual is None) or (q is None) == quant or (qs is None) == quant:
             raise ValueError("out must hold (y, s, q, q_scale), None exactly where nothing is returned")
-    if residual is not None:
-        pr, ldr = _rows("residual", residual, T, H, dt, dev)
-        pso, ldso = _rows("out s", s, T, H, dt, dev)
-    if weight is not None:
-        pw = _vector("weight", weight, H, dt, dev)
-    if norm:
-        py, ldy = _rows("out y", y, T, H, dt, dev)
-    if quant:
-        pq, ldq = _rows("out q", q, T, H, _E4M3, dev)
-        pqs = _vector("out q_scale", qs, T, _F32, dev)
-    cfg = _config(RmsnormConfig, _DTYPES[dt], H, eps, 0, ldx, ldr, ldso, ldy, ldq)[1]
-    _call(_lib().moe_w4a16_add_rmsnorm, stream, dev, cfg, T, px, pr, pw, pso, py, pq, pqs)
+    (_native or _load()).add_rmsnorm(x, residual, weight, eps, y, s, q, qs, stream)
     return y, s, q, qs
 
 
@@ -159,22 +115,16 @@ def route_scored(logits, top_k: int, *, score: str = "softmax", bias=None, group
     the largest sum of their `group_rank` (1 or 2) largest choices stay
     eligible; the weights are the scores of the chosen, divided by their sum
     if renormalize, times scale.  out: (ids, weights) to be written."""
-    dev = _input("logits", logits, _LOGIT_TYPES)
-    T, E = logits.shape
-    if score not in _SCORES:
+    code = _SCORES.get(score)
+    if code is None:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
-    pl, ld = _rows("logits", logits, T, E, logits.dtype, dev)
     if out is None:
-        ids, w = _empty((T, top_k), _I32, logits, stream), _empty((T, top_k), _F32, logits, stream)
+        shape = (logits.shape[0], top_k)
+        ids, w = _empty(shape, _I32, logits, stream), _empty(shape, _F32, logits, stream)
     else:
         ids, w = out
-    for name, t, d in (("out ids", ids, _I32), ("out weights", w, _F32)):
-        if _rows(name, t, T, top_k, d, dev)[1] != top_k:
-            raise ValueError(f"{name} must be contiguous")
-    pb = _vector("bias", bias, E, _F32, dev) if bias is not None else 0
-    cfg = _config(RouteConfig, _DTYPES[logits.dtype], E, top_k, _SCORES[score], groups, top_groups, group_rank,
-                  int(bool(renormalize)), scale, 0, ld)[1]
-    _call(_lib().moe_w4a16_route_scored, stream, dev, cfg, T, pl, pb, ids.data_ptr(), w.data_ptr())
+    (_native or _load()).route_scored(logits, bias, ids, w, top_k, code, groups, top_groups, group_rank, renormalize,
+                                      scale, stream)
     return ids, w
 
 
@@ -187,38 +137,15 @@ def linear(x, w, *, bias=None, act: str = "none", residual=None, x_scale=None, w
     then N up rows; silu(gate) * up).  The output [T, N] has out_dtype (x's
     type; fp16 for E4M3), fp16, bf16 or fp32, like the residual; it may be
     the residual."""
-    dev = _input("x", x, _LINEAR_TYPES)
-    T, K = x.shape
-    dt = x.dtype
     code = _ACTS.get(act)
     if code is None:
         raise ValueError("act must be one of " + ", ".join(_ACTS))
-    M = w.shape[0]
-    if code == 5 and M % 2:
-        raise ValueError("swiglu needs an even number of rows in w")
-    N = M // 2 if code == 5 else M
-    px, ldx = _rows("x", x, T, K, dt, dev)
-    pw, ldw = _rows("w", w, M, K, dt, dev)
     if out is None:
-        out = _empty((T, N), out_dtype or (torch.float16 if dt is _E4M3 else dt), x, stream)
+        n = w.shape[0] // 2 if code == 5 else w.shape[0]
+        out = _empty((x.shape[0], n), out_dtype or (torch.float16 if x.dtype is _E4M3 else x.dtype), x, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError("out has another type than out_dtype")
-    ot = out.dtype
-    if ot not in _LOGIT_TYPES:
-        raise ValueError("the output must be fp16, bf16 or fp32")
-    po, ldo = _rows("out", out, T, N, ot, dev)
-    pb = _vector("bias", bias, M, _F32, dev) if bias is not None else 0
-    pr = ldr = pxs = pws = 0
-    if residual is not None:
-        pr, ldr = _rows("residual", residual, T, N, ot, dev)
-    if dt is _E4M3:
-        if x_scale is None or w_scale is None:
-            raise ValueError("E4M3 needs x_scale and w_scale")
-        pxs, pws = _vector("x_scale", x_scale, T, _F32, dev), _vector("w_scale", w_scale, M, _F32, dev)
-    elif x_scale is not None or w_scale is not None:
-        raise ValueError("x_scale and w_scale go with E4M3 only")
-    cfg = _config(LinearConfig, _DTYPES[dt], _DTYPES[ot], N, K, code, 0, ldx, ldw, ldr, ldo)[1]
-    _call(_lib().moe_w4a16_linear, stream, dev, cfg, T, px, pw, pxs, pws, pb, pr, po)
+    (_native or _load()).linear(x, w, x_scale, w_scale, bias, residual, out, code, stream)
     return out
 
 

@@ -248,6 +248,17 @@ def test_linear_shapes(T, N, K, dtype, out):
     check_linear(*t, "none", B.linear(t[0], t[1], out_dtype=out))
 
 
+@pytest.mark.parametrize("T", [1, 16, 30, 61, 100])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("N,K", [(4096, 3000), (12000, 1536), (20, 20000)])
+def test_linear_every_pipeline_stage(T, act, N, K):
+    """Enough K chunks per CTA to go round the ring, with few and many tiles."""
+    for dtype in (F16, E4):
+        t = make_linear(T, N, K // 16 * 16, dtype, act, False, False, F16, T)
+        x, w, xs, ws, _, _ = t
+        check_linear(*t, act, B.linear(x, w, act=act, x_scale=xs, w_scale=ws, out_dtype=F16))
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 100, 16), (5, 64, 2048), (40, 129, 272), (130, 300, 1024)])
 @pytest.mark.parametrize("out", [F16, BF16, F32], ids=["fp16", "bf16", "fp32"])
 @pytest.mark.parametrize("act", ["none", "swiglu"])

@@ -4,14 +4,20 @@
 // 128 8-bit values and one MMA takes 32 bytes of it, so the pipeline is the
 // same for all three.
 //
-// linear_narrow_kernel: W is the MMA's A operand (128 weight rows, M), the
-// tokens are N (16, 32, 64 or 128 of them), so a few tokens waste little of
-// the tensor core and the kernel streams W.  The K chunks of a tile are split
-// over the S CTAs of a cluster; every CTA leaves its FP32 part in its own
-// shared memory and the parts are added in rank order through distributed
-// shared memory, each CTA finishing its share of the tile (no workspace, no
-// atomics, one launch).  For SWIGLU the 128 rows are 64 gate rows and the
-// matching 64 up rows.
+// linear_narrow_kernel (up to 64 tokens; bound by reading W once): W is the
+// MMA's A operand (128 weight rows, M), the tokens are N (16, 32 or 64 of
+// them), so a few tokens waste little of the tensor core.  The K chunks of a
+// tile are split over the S CTAs of a cluster; every CTA sends its FP32 part
+// of a token's row to that token's owner in the cluster, which adds the parts
+// in rank order and finishes the row (no workspace, no atomics, one launch).
+// For SWIGLU the 128 rows are 64 gate rows and the matching 64 up rows.
+// W [11264][2048] FP16, one token: 9.9 us, 4.7 TB/s.
+//
+// linear_wide_kernel (more tokens; bound by the tensor cores, or by the few
+// tiles of a short problem): persistent CTA pairs (cta_group::2) over tiles
+// of 256 tokens x 256, 128 or 64 weight rows, two accumulators, so that one
+// tile's epilogue runs under the next tile's MMAs.
+// T = 2048, W [11264][2048]: E4M3 37 us (2,550 TFLOP/s), FP16 56 us (1,690).
 #include <cuda.h>
 
 #include "block.h"
@@ -29,49 +35,204 @@ struct LinearArgs {
   long long ld_res, ld_out;
   int T, N, K;       // K in elements
   int act;
-  uint32_t idesc;    // MMA instruction descriptor without its N field
+  uint32_t idesc;    // MMA instruction descriptor without its M and N fields
   int vec;           // 4: four neighbouring outputs can be read and written at once, else 1
 };
 
-DEV_INLINE float gelu_tanh(float a) { return 0.5f * a * (1.f + tanhf(0.7978845608f * (a + 0.044715f * a * a * a))); }
-
-DEV_INLINE float activate(float a, int act) {
+// The switch stands outside the values' loop: one branch per value kept a
+// thread's values from overlapping (a 256 x 256 tile's epilogue took 7.5 us).
+template <int N>
+DEV_INLINE void activate(float (&v)[N], int act) {
   switch (act) {
-    case MOE_W4A16_ACT_RELU: return a > 0.f ? a : (a == a ? 0.f : a);
-    case MOE_W4A16_ACT_GELU: return 0.5f * a * (1.f + erff(a * 0.70710678f));
-    case MOE_W4A16_ACT_GELU_TANH: return gelu_tanh(a);
-    case MOE_W4A16_ACT_SILU: return a / (1.f + __expf(-a));
-    default: return a;
+    case MOE_W4A16_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];   // NaN stays
+      break;
+    case MOE_W4A16_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * (1.f + erff(v[i] * 0.70710678f));
+      break;
+    case MOE_W4A16_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        v[i] = 0.5f * v[i] * (1.f + tanhf(0.7978845608f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
+      break;
+    case MOE_W4A16_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = v[i] / (1.f + __expf(-v[i]));
+      break;
+    default: break;
   }
 }
 
-template <bool F8>
-DEV_INLINE void umma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
-  if (F8)
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
-        : "memory");
-  else
-    umma_f16_ss(d_tmem, a_desc, b_desc, idesc, acc);
+// The warp that issues the MMAs runs converged, every lane with the same
+// values, and one elected lane executes the instruction: descriptors and
+// addresses then live in uniform registers.  Inside an `if (lane == 0)` each
+// MMA cost 75 cycles of issue, whatever its N.
+DEV_INLINE uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
 }
 
-// Four neighbouring outputs of a row: residual and store, V of them valid.
-template <typename O>
-DEV_INLINE void finish4(const LinearArgs& a, int t, int n, const float (&v)[4]) {
-  O* op = static_cast<O*>(a.out) + (size_t)t * a.ld_out + n;
-  const O* rp = a.res ? static_cast<const O*>(a.res) + (size_t)t * a.ld_res + n : nullptr;
-  if (a.vec == 4 && n + 4 <= a.N) {
-    blk::Pack<O, 4> o, r;
-    if (rp) r = *reinterpret_cast<const blk::Pack<O, 4>*>(rp);
+#define UMMA_ASM(group, kind)                                                                       \
+  asm volatile(                                                                                     \
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"                      \
+      " @q tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem), \
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc), "r"(leader)                                   \
+      : "memory")
+
+template <bool F8, int GROUP>
+DEV_INLINE void umma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc,
+                     uint32_t leader) {
+  if constexpr (GROUP == 1 && F8) UMMA_ASM("1", "f8f6f4");
+  else if constexpr (GROUP == 1) UMMA_ASM("1", "f16");
+  else if constexpr (F8) UMMA_ASM("2", "f8f6f4");
+  else UMMA_ASM("2", "f16");
+}
+
+// Arrives on `bar` once the MMAs issued so far are done; the pair form at its
+// place in both CTAs.
+DEV_INLINE void commit_one(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+DEV_INLINE void commit_pair(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+      " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3), "r"(leader)
+      : "memory");
+}
+
+// The same for the warp that loads: the elected lane expects `bytes` and fetches.
+DEV_INLINE void expect_bytes(uint32_t bar, uint32_t bytes, uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+      " @q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar),
+      "r"(bytes), "r"(leader)
+      : "memory");
+}
+// TMA box -> this CTA's shared memory; GROUP 2: counted by the barrier at the
+// cluster address `bar`, in either CTA of the pair.
+template <int GROUP>
+DEV_INLINE void fetch(uint32_t dst, const CUtensorMap* tmap, int c0, int r0, uint32_t bar, uint32_t leader) {
+  if constexpr (GROUP == 1)
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n"
+        " @q cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(r0), "r"(bar), "r"(leader)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n"
+        " @q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(r0), "r"(bar), "r"(leader)
+        : "memory");
+}
+
+DEV_INLINE void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
+// The end of the epilogue for Q quads of outputs: quad q holds the columns n,
+// n + step, .. n + 3 step of token t[q] (step 1: neighbours, read and written
+// at once).  live[q] says whether the quad exists.  Written without branches
+// per quad: each cost a thread 50-100 cycles, and a 256 x 256 tile's
+// epilogue 7.5 us.
+template <typename O, int Q>
+DEV_INLINE void store_quads(const LinearArgs& a, const int (&t)[Q], const bool (&live)[Q], int n, int step,
+                            const float (&v)[Q * 4]) {
+  O* const out = static_cast<O*>(a.out);
+  const O* const res = static_cast<const O*>(a.res);
+  if (step == 1) {
+    blk::Pack<O, 4> o[Q];
+    if (res) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o.v[i] = blk::from_float<O>(rp ? v[i] + blk::to_float(r.v[i]) : v[i]);
-    *reinterpret_cast<blk::Pack<O, 4>*>(op) = o;
+      for (int q = 0; q < Q; ++q)
+        if (live[q]) o[q] = *reinterpret_cast<const blk::Pack<O, 4>*>(res + (size_t)t[q] * a.ld_res + n);
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[q].v[j] = blk::from_float<O>(v[4 * q + j] + blk::to_float(o[q].v[j]));
+    } else {
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[q].v[j] = blk::from_float<O>(v[4 * q + j]);
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (live[q]) *reinterpret_cast<blk::Pack<O, 4>*>(out + (size_t)t[q] * a.ld_out + n) = o[q];
   } else {
+    bool in[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < a.N) op[i] = blk::from_float<O>(rp ? v[i] + blk::to_float(rp[i]) : v[i]);
+    for (int j = 0; j < 4; ++j) in[j] = n + j * step < a.N;
+    O o[Q * 4];
+    if (res) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (live[q] && in[j]) o[4 * q + j] = res[(size_t)t[q] * a.ld_res + n + j * step];
+#pragma unroll
+      for (int i = 0; i < Q * 4; ++i) o[i] = blk::from_float<O>(v[i] + blk::to_float(o[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < Q * 4; ++i) o[i] = blk::from_float<O>(v[i]);
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (live[q] && in[j]) out[(size_t)t[q] * a.ld_out + n + j * step] = o[4 * q + j];
+  }
+}
+
+// Scales, bias and activation of quads whose columns are n + j step; g holds
+// the (gate) sums, u the up sums, already times the token's x_scale.
+template <bool GATED, int Q>
+DEV_INLINE void activate_quads(const LinearArgs& a, int n, int step, float (&g)[Q * 4], float (&u)[GATED ? Q * 4 : 1]) {
+  int nn[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) nn[j] = min(n + j * step, a.N - 1);
+  if (a.ws) {
+    float w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = a.ws[nn[j]];
+#pragma unroll
+    for (int i = 0; i < Q * 4; ++i) g[i] *= w[i % 4];
+    if constexpr (GATED) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = a.ws[a.N + nn[j]];
+#pragma unroll
+      for (int i = 0; i < Q * 4; ++i) u[i] *= w[i % 4];
+    }
+  }
+  if (a.bias) {
+    float b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = a.bias[nn[j]];
+#pragma unroll
+    for (int i = 0; i < Q * 4; ++i) g[i] += b[i % 4];
+    if constexpr (GATED) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = a.bias[a.N + nn[j]];
+#pragma unroll
+      for (int i = 0; i < Q * 4; ++i) u[i] += b[i % 4];
+    }
+  }
+  if constexpr (GATED) {
+#pragma unroll
+    for (int i = 0; i < Q * 4; ++i) g[i] = __fdividef(g[i], 1.f + __expf(-g[i])) * u[i];
+  } else {
+    activate(g, a.act);
   }
 }
 
@@ -90,16 +251,28 @@ struct Pipe {   // stage index and phase parity of a ring
 template <int NT>
 struct NarrowCfg {
   static constexpr int kA = 128 * kChunk, kB = NT * kChunk, kStage = kA + kB;
-  static constexpr int kStages = (104 * 1024) / kStage;   // two CTAs per SM
-  static constexpr int kPart = NT * 128 * 4;              // FP32 part of the tile, over the stages when they are done
-  static constexpr int kRing = kStages * kStage > kPart ? kStages * kStage : kPart;
-  static constexpr int kSmem = kRing + (2 * kStages + 1) * 8 + 16 + 1024;
+  // The parts that this CTA receives, [sending rank][token][row]: at most 7
+  // tokens' room is lost to rounding.  Up to 32 tokens they have a place of
+  // their own, so that a CTA can send before the receiver has finished; for
+  // 64 they go over the stages.
+  static constexpr int kRecv = (NT + 7) * 128 * 4;
+  static constexpr bool kOwnRecv = NT <= 32;
+  static constexpr int kBudget = 110 * 1024;   // two CTAs per SM
+  static constexpr int kStages = (kBudget - (kOwnRecv ? kRecv : 0)) / kStage;
+  static constexpr int kRing = kStages * kStage;
+  static_assert(kOwnRecv || kRecv <= kRing, "the parts fit over the stages");
+  static constexpr int kRecvAt = kOwnRecv ? kRing : 0;
+  static constexpr int kBarAt = kRing + (kOwnRecv ? kRecv : 0);
+  static constexpr int kSmem = kBarAt + (2 * kStages + 1) * 8 + 16 + 1024;
   static constexpr uint32_t kCols = NT < 32 ? 32 : NT;
   static constexpr int kThreads = 192;   // warp 0 loads, warp 1 multiplies, warps 2-5 empty the accumulator
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
-template <bool F8, int NT>
+DEV_INLINE void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+DEV_INLINE void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+template <bool F8, bool GATED, int NT>
 __global__ void __launch_bounds__(192, 2)
     linear_narrow_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ CUtensorMap tmW,
                          const __grid_constant__ CUtensorMap tmX, int out_dtype, int S) {
@@ -107,21 +280,26 @@ __global__ void __launch_bounds__(192, 2)
   constexpr int kElem = F8 ? 128 : 64;   // K values per chunk
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarAt);
   uint64_t* empty = full + C::kStages;
   uint64_t* done = empty + C::kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool gated = a.act == MOE_W4A16_ACT_SWIGLU;
-  const int FT = gated ? 64 : 128;   // output features per tile
+  constexpr int FT = GATED ? 64 : 128;   // output features per tile
   // the CTAs of a cluster are neighbours in x; then the token tiles of one
   // weight tile, so that W comes from L2 after its first reader
   const int rank = blockIdx.x % S, tile = blockIdx.x / S;
   const int ntt = (a.T + NT - 1) / NT;
   const int t0 = (tile % ntt) * NT, n0 = (tile / ntt) * FT;
   const int nk = (a.K + kElem - 1) / kElem;
-  const int k0 = (int)((long long)nk * rank / S), k1 = (int)((long long)nk * (rank + 1) / S);
+  // rank r takes the chunks r, r + S, ..: the cluster reads neighbouring
+  // 128-byte pieces of a weight row at about the same time
+  const int mine = (nk - rank + S - 1) / S;
 
+  if (threadIdx.x == 32) {
+    prefetch_map(&tmW);
+    prefetch_map(&tmX);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -130,9 +308,6 @@ __global__ void __launch_bounds__(192, 2)
     mbar_init(done, 1);
     fence_mbar_init();
   }
-  // tensor memory is taken after the wait and before the trigger: no grid
-  // holds any while it waits for one that still has to allocate
-  pdl_wait();
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::kCols);
     tmem_relinquish();
@@ -141,124 +316,394 @@ __global__ void __launch_bounds__(192, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // The trigger comes after the allocation: the next grid starts only when
+  // every CTA of this one has its tensor memory, so a CTA that holds some
+  // while it waits here never keeps the grid before from getting its own.
+  pdl_wait();
   pdl_trigger();
+  if (C::kOwnRecv && S > 1) cluster_arrive();   // this CTA runs: its place for parts can be written
 
+  bool ok = true;
   if (warp == 0) {
-    if (lane == 0) {
-      Pipe p;
-      int k = k0;
-      for (; k < k1; ++k) {
-        if (!mbar_wait_bounded(&empty[p.i], p.ph ^ 1u, &g_block_status)) break;
-        uint8_t* dst = smem + p.i * C::kStage;
-        mbar_expect_tx(&full[p.i], (uint32_t)C::kStage);
-        if (gated) {
-          tma_load_2d(dst, &tmW, k * kElem, n0, &full[p.i]);
-          tma_load_2d(dst + 64 * kChunk, &tmW, k * kElem, a.N + n0, &full[p.i]);
-        } else {
-          tma_load_2d(dst, &tmW, k * kElem, n0, &full[p.i]);
-        }
-        tma_load_2d(dst + C::kA, &tmX, k * kElem, t0, &full[p.i]);
-        p.next(C::kStages);
-      }
-      if (k < k1) {   // gave up: the copies in flight land before the CTA ends
-        const int issued = k - k0;
-        for (int s = 0; s < C::kStages && s < issued; ++s) {
-          const int last = s + (issued - 1 - s) / C::kStages * C::kStages;
-          mbar_wait_bounded(&full[s], (uint32_t)((last / C::kStages) & 1), &g_block_status);
-        }
+    Pipe p;
+    const uint32_t leader = elect_lane(), ring = smem_u32(smem), bars = smem_u32(full);
+    int issued = 0;
+    for (; issued < mine; ++issued) {
+      if (!mbar_wait_bounded(&empty[p.i], p.ph ^ 1u, &g_block_status)) break;
+      const int c0 = (rank + issued * S) * kElem;
+      const uint32_t dst = ring + (uint32_t)(p.i * C::kStage), bar = bars + (uint32_t)(p.i * 8);
+      expect_bytes(bar, (uint32_t)C::kStage, leader);
+      fetch<1>(dst, &tmW, c0, n0, bar, leader);
+      if (GATED) fetch<1>(dst + FT * kChunk, &tmW, c0, a.N + n0, bar, leader);
+      fetch<1>(dst + C::kA, &tmX, c0, t0, bar, leader);
+      p.next(C::kStages);
+    }
+    if (issued < mine) {   // gave up: the copies in flight land before the CTA ends
+      for (int s = 0; s < C::kStages && s < issued; ++s) {
+        const int last = s + (issued - 1 - s) / C::kStages * C::kStages;
+        mbar_wait_bounded(&full[s], (uint32_t)((last / C::kStages) & 1), &g_block_status);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      Pipe p;
-      const uint32_t idesc = a.idesc | ((uint32_t)(NT >> 3) << 17);
-      for (int k = k0; k < k1; ++k) {
-        if (!mbar_wait_bounded(&full[p.i], p.ph, &g_block_status)) break;
-        tc_fence_after();
-        const uint32_t base = smem_u32(smem + p.i * C::kStage);
-        const uint64_t ad = sw128_desc(base), bd = sw128_desc(base + C::kA);
+    Pipe p;
+    const uint32_t leader = elect_lane();
+    const uint32_t idesc = a.idesc | ((uint32_t)(NT >> 3) << 17) | ((128u >> 4) << 24);
+    const uint32_t d = __reduce_or_sync(0xffffffffu, tmem);   // the same in every lane, and known to be
+    const uint64_t desc0 = sw128_desc(smem_u32(smem));        // its address field counts 16 bytes
+    for (int k = 0; k < mine; ++k) {
+      if (!mbar_wait_bounded(&full[p.i], p.ph, &g_block_status)) break;
+      tc_fence_after();
+      const uint64_t ad = desc0 + (uint64_t)(p.i * (C::kStage / 16)), bd = ad + C::kA / 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)   // 32 bytes of K each; the address field counts 16 bytes
-          umma<F8>(tmem, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (uint32_t)(k > k0 || j > 0));
-        umma_commit(&empty[p.i]);
-        p.next(C::kStages);
-      }
-      umma_commit(done);
+      for (int j = 0; j < 4; ++j)   // 32 bytes of K each
+        umma<F8, 1>(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (uint32_t)((k | j) != 0), leader);
+      commit_one(&empty[p.i], leader);
+      p.next(C::kStages);
     }
+    commit_one(done, leader);
     __syncwarp();
   } else {
-    // the accumulator -> this CTA's part [token][weight row]; every stage has
-    // been consumed once `done` completes
-    const bool ok = mbar_wait_bounded(done, 0, &g_block_status);
-    tc_fence_after();
+    ok = mbar_wait_bounded(done, 0, &g_block_status);   // every stage has been consumed
+    __syncwarp();
+  }
+
+  // Token c of the tile belongs to rank c % S: every CTA sends its part of c's
+  // row there, as slot c / S, and the owner adds the parts in rank order.
+  if (S > 1) {
+    if (!C::kOwnRecv) cluster_arrive();   // this CTA's stages are free
+    cluster_wait();
+  } else if (!C::kOwnRecv) {
+    __syncthreads();
+  }
+  const int nt = min(NT, a.T - t0), cap = (NT + S - 1) / S;
+  const uint32_t recv = smem_u32(smem + C::kRecvAt);
+  if (warp >= 2) {
     const int q = warp & 3, row = q * 32 + lane;
-    float* part = reinterpret_cast<float*>(smem) + row;
-    const int nt = min(NT, a.T - t0);
-    if (ok)
+    tc_fence_after();
+    if (ok) {
+      int owner = 0;
+      uint32_t at = recv + (uint32_t)((rank * cap * 128 + row) * 4);
       for (int c0 = 0; c0 < nt; c0 += 16) {
         uint32_t v[16];
         tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c0 + j) * 128] = __uint_as_float(v[j]);
+        for (int j = 0; j < 16; ++j) {
+          if (c0 + j < nt) {
+            uint32_t addr;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(at), "r"(owner));
+            st_cluster_f32(addr, __uint_as_float(v[j]));
+          }
+          if (++owner == S) {
+            owner = 0;
+            at += 512;
+          }
+        }
       }
+    }
     tc_fence_before();
   }
-  __syncthreads();
+  __syncwarp();
+  if (S > 1) cluster_sync();
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
-  if (S > 1) cluster_sync();
 
-  // four neighbouring features of a token at a time, spread over the cluster
-  const int nt = min(NT, a.T - t0), fq = FT / 4;
-  const uint32_t part = smem_u32(smem);
-  for (int i = rank * C::kThreads + threadIdx.x; i < nt * fq; i += S * C::kThreads) {
-    const int tt = i / fq, f = (i % fq) * 4, t = t0 + tt, n = n0 + f;
-    if (n >= a.N) continue;
-    float v[2][4] = {};
-    const uint32_t off = part + (uint32_t)(tt * 128 + f) * 4u;
-    for (int r = 0; r < S; ++r) {
+  // The quads of this CTA's tokens: neighbouring columns where the output
+  // allows wide stores, else kQ apart, so that the lanes' single stores still
+  // lie side by side.  A thread's quads are of one column group.
+  constexpr int kQ = FT / 4, kBatch = NT > 16 ? 2 : 1, kSweep = C::kThreads / kQ;
+  static_assert(C::kThreads % kQ == 0, "a thread keeps its columns");
+  const bool wide = a.vec == 4 && n0 + FT <= a.N;
+  const int step = wide ? 1 : kQ, f = (int)(threadIdx.x % kQ) * (wide ? 4 : 1), n = n0 + f;
+  const int own = (nt - rank + S - 1) / S;   // tokens of this CTA
+  const float* parts = reinterpret_cast<const float*>(smem + C::kRecvAt) + f;
+  if (n < a.N)
+    for (int s = (int)threadIdx.x / kQ; s < own; s += kSweep * kBatch) {
+      int t[kBatch];
+      bool live[kBatch];
+      float v[kBatch * 4] = {}, up[GATED ? kBatch * 4 : 1] = {};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h == 1 && !gated) break;
-        uint32_t addr;
-        float p0, p1, p2, p3;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(off + h * 256u), "r"(r));
-        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(p0), "=f"(p1), "=f"(p2), "=f"(p3)
-                     : "r"(addr)
-                     : "memory");
-        v[h][0] += p0;
-        v[h][1] += p1;
-        v[h][2] += p2;
-        v[h][3] += p3;
+      for (int q = 0; q < kBatch; ++q) {
+        const int sl = s + q * kSweep;
+        live[q] = sl < own;
+        t[q] = t0 + min(sl, own - 1) * S + rank;
+        const float* p = parts + min(sl, own - 1) * 128;
+        if (wide) {
+#pragma unroll 4
+          for (int r = 0; r < S; ++r, p += cap * 128) {
+            const float4 g = *reinterpret_cast<const float4*>(p);
+            v[4 * q] += g.x, v[4 * q + 1] += g.y, v[4 * q + 2] += g.z, v[4 * q + 3] += g.w;
+            if constexpr (GATED) {
+              const float4 h = *reinterpret_cast<const float4*>(p + FT);
+              up[4 * q] += h.x, up[4 * q + 1] += h.y, up[4 * q + 2] += h.z, up[4 * q + 3] += h.w;
+            }
+          }
+        } else {
+#pragma unroll 4
+          for (int r = 0; r < S; ++r, p += cap * 128)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[4 * q + j] += p[j * kQ];
+              if constexpr (GATED) up[4 * q + j] += p[FT + j * kQ];
+            }
+        }
+        if (a.xs) {
+          const float xs = a.xs[t[q]];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[4 * q + j] *= xs;
+            if constexpr (GATED) up[4 * q + j] *= xs;
+          }
+        }
+      }
+      activate_quads<GATED, kBatch>(a, n, step, v, up);
+      if (out_dtype == MOE_W4A16_F16) store_quads<__half, kBatch>(a, t, live, n, step, v);
+      else if (out_dtype == MOE_W4A16_BF16) store_quads<__nv_bfloat16, kBatch>(a, t, live, n, step, v);
+      else store_quads<float, kBatch>(a, t, live, n, step, v);
+    }
+}
+
+// -------------------------------------------------------------------- wide
+// A pair of CTAs shares one tile of 256 tokens x BN weight rows: each loads
+// its 128 token rows and half of the weight rows, the first issues the MMAs of
+// both, and each finishes its 128 tokens.
+template <int BN>
+struct WideCfg {
+  static constexpr int kA = 128 * kChunk;   // the 128 token rows of this CTA
+  static constexpr int kB = BN / 2 * kChunk;   // this CTA's half of the weight rows
+  static constexpr int kStage = kA + kB;
+  static constexpr int kStages = 192 * 1024 / kStage;
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kTurn = 32 * 32 * 4;   // per epilogue warp: 32 rows x 32 FP32 columns
+  static constexpr int kBars = 2 * kStages + 4;
+  static constexpr int kSmem = kStages * kStage + kEpiWarps * kTurn + kBars * 8 + 16 + 1024;
+  static constexpr int kThreads = (2 + kEpiWarps) * 32;   // warp 0 loads, warp 1 multiplies, the others finish
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+};
+
+// 32 rows of one warp, turned: `buf` holds [32 rows][8 units of 4 columns] with
+// unit u of row r at u ^ (r & 7), so that neither the writes (a row per lane)
+// nor the reads (8 lanes along a row) meet in a bank.  GATED: units 0-3 are
+// gate, 4-7 the matching up columns, 4 lanes a row.  A lane finishes 4
+// columns of 8 (GATED: 4) rows, 64- or 128-byte pieces of a row per store;
+// outputs that cannot be stored four at a time have a lane's columns
+// kLanes apart, so that the lanes' single stores still lie side by side.
+template <bool GATED, typename O>
+DEV_INLINE void finish_turned(const LinearArgs& a, const float* buf, int t0, int n0, int lane) {
+  constexpr int kLanes = GATED ? 4 : 8;    // lanes along a row
+  constexpr int kPass = GATED ? 4 : 8, kRows = 32 / kPass;
+  const bool wide = a.vec == 4 && n0 + 4 * kLanes <= a.N;
+  const int u = lane % kLanes, step = wide ? 1 : kLanes, c = wide ? 4 * u : u;
+  // rows of a pass; GATED: neighbours in a quarter warp are 4 rows apart, else
+  // their units would share banks
+  const int i = lane / kLanes, r0 = GATED ? (i >> 1) + (i & 1) * 4 : i;
+  float v[kPass * 4], w[GATED ? kPass * 4 : 1];
+  if (wide) {
+#pragma unroll
+    for (int p = 0; p < kPass; ++p) {
+      const int r = r0 + p * kRows;
+      const float4 g = *reinterpret_cast<const float4*>(buf + r * 32 + ((u ^ (r & 7)) * 4));
+      v[4 * p] = g.x, v[4 * p + 1] = g.y, v[4 * p + 2] = g.z, v[4 * p + 3] = g.w;
+      if constexpr (GATED) {
+        const float4 h = *reinterpret_cast<const float4*>(buf + r * 32 + (((u + 4) ^ (r & 7)) * 4));
+        w[4 * p] = h.x, w[4 * p + 1] = h.y, w[4 * p + 2] = h.z, w[4 * p + 3] = h.w;
       }
     }
-    const float xs = a.xs ? a.xs[t] : 1.f;
-    float o[4];
+  } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int nn = min(n + j, a.N - 1);
-      float g = v[0][j];
-      if (a.ws) g *= xs * a.ws[nn];
-      if (a.bias) g += a.bias[nn];
-      if (gated) {
-        float u = v[1][j];
-        if (a.ws) u *= xs * a.ws[a.N + nn];
-        if (a.bias) u += a.bias[a.N + nn];
-        o[j] = g / (1.f + __expf(-g)) * u;
-      } else {
-        o[j] = activate(g, a.act);
+    for (int p = 0; p < kPass; ++p) {
+      const int r = r0 + p * kRows;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int cc = c + j * step;
+        v[4 * p + j] = buf[r * 32 + (((cc >> 2) ^ (r & 7)) * 4) + (cc & 3)];
+        if constexpr (GATED) w[4 * p + j] = buf[r * 32 + ((((cc >> 2) + 4) ^ (r & 7)) * 4) + (cc & 3)];
       }
     }
-    if (out_dtype == MOE_W4A16_F16) finish4<__half>(a, t, n, o);
-    else if (out_dtype == MOE_W4A16_BF16) finish4<__nv_bfloat16>(a, t, n, o);
-    else finish4<float>(a, t, n, o);
   }
-  if (S > 1) cluster_sync();   // nobody leaves while its part is read
+  activate_quads<GATED, kPass>(a, n0 + c, step, v, w);
+  int t[kPass];
+  bool live[kPass];
+#pragma unroll
+  for (int p = 0; p < kPass; ++p) {
+    t[p] = t0 + r0 + p * kRows;
+    live[p] = t[p] < a.T;
+  }
+  store_quads<O, kPass>(a, t, live, n0 + c, step, v);
+}
+
+template <bool F8, bool GATED, int BN, typename O>
+__global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
+    linear_wide_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ CUtensorMap tmW,
+                       const __grid_constant__ CUtensorMap tmX) {
+  using C = WideCfg<BN>;
+  constexpr int kElem = F8 ? 128 : 64;
+  constexpr uint32_t kCols = 2 * BN;      // two accumulators
+  constexpr int FT = GATED ? BN / 2 : BN;   // output features per tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  float* turn = reinterpret_cast<float*>(smem + C::kStages * C::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStage + C::kEpiWarps * C::kTurn);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* acc_full = empty + C::kStages;   // [2]
+  uint64_t* acc_empty = acc_full + 2;        // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int mtiles = (a.T + 255) / 256;
+  const int tiles = mtiles * ((a.N + FT - 1) / FT);
+  const int nk = (a.K + kElem - 1) / kElem;
+  const int first = blockIdx.x / 2, step = gridDim.x / 2;
+
+  if (threadIdx.x == 32) {
+    prefetch_map(&tmW);
+    prefetch_map(&tmX);
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&acc_full[s], 1);
+      mbar_init(&acc_empty[s], 2 * C::kEpiWarps);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the peer's barriers are ready
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();   // after the allocation: see the narrow kernel
+  pdl_trigger();
+
+  if (warp == 0) {
+    Pipe p;
+    bool ok = true;
+    int issued = 0;
+    const uint32_t leader = elect_lane(), ring = smem_u32(smem), bars = smem_u32(full), bars0 = map_to_rank(full, 0);
+    for (int tile = first; tile < tiles && ok; tile += step) {
+      const int m0 = (tile % mtiles) * 256 + rank * 128, n0 = (tile / mtiles) * FT;
+      const int b0 = rank == 0 ? n0 : GATED ? a.N + n0 : n0 + BN / 2;   // this CTA's weight rows
+      for (int k = 0; k < nk; ++k) {
+        if (!mbar_wait_bounded(&empty[p.i], p.ph ^ 1u, &g_block_status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = ring + (uint32_t)(p.i * C::kStage), bar0 = bars0 + (uint32_t)(p.i * 8);
+        if (rank == 0) expect_bytes(bars + (uint32_t)(p.i * 8), (uint32_t)(2 * C::kStage), leader);
+        fetch<2>(dst, &tmX, k * kElem, m0, bar0, leader);
+        fetch<2>(dst + C::kA, &tmW, k * kElem, b0, bar0, leader);
+        ++issued;
+        p.next(C::kStages);
+      }
+    }
+    if (!ok && rank == 0) {   // gave up: the copies in flight land before the CTAs end
+      for (int s = 0; s < C::kStages && s < issued; ++s) {
+        const int last = s + (issued - 1 - s) / C::kStages * C::kStages;
+        mbar_wait_bounded(&full[s], (uint32_t)((last / C::kStages) & 1), &g_block_status);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      Pipe p, acc;
+      bool ok = true;
+      const uint32_t leader = elect_lane();
+      const uint32_t idesc = a.idesc | ((uint32_t)(BN >> 3) << 17) | ((256u >> 4) << 24);
+      const uint32_t tm = __reduce_or_sync(0xffffffffu, tmem);
+      const uint64_t desc0 = sw128_desc(smem_u32(smem));
+      for (int tile = first; tile < tiles && ok; tile += step) {
+        if (!mbar_wait_bounded(&acc_empty[acc.i], acc.ph ^ 1u, &g_block_status)) break;
+        tc_fence_after();
+        const uint32_t d = tm + (uint32_t)(acc.i * BN);
+        for (int k = 0; k < nk; ++k) {
+          if (!mbar_wait_bounded(&full[p.i], p.ph, &g_block_status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = desc0 + (uint64_t)(p.i * (C::kStage / 16)), bd = ad + C::kA / 16;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            umma<F8, 2>(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (uint32_t)((k | j) != 0), leader);
+          commit_pair(&empty[p.i], leader);
+          p.next(C::kStages);
+        }
+        if (ok) commit_pair(&acc_full[acc.i], leader);
+        acc.next(2);
+      }
+    }
+    __syncwarp();
+  } else {
+    // a TMEM lane (token) per thread; the two warps of a lane quarter take half
+    // of the tile's output features each
+    const int q = warp & 3, h = (warp - 2) >> 2;
+    float* buf = turn + (warp - 2) * (C::kTurn / 4);
+    Pipe acc;
+    for (int tile = first; tile < tiles; tile += step) {
+      if (!mbar_wait_bounded(&acc_full[acc.i], acc.ph, &g_block_status)) break;
+      tc_fence_after();
+      const int t0 = (tile % mtiles) * 256 + rank * 128 + q * 32, n0 = (tile / mtiles) * FT;
+      const uint32_t d = tmem + (uint32_t)(acc.i * BN) + ((uint32_t)(q * 32) << 16);
+      const float xs = a.xs && t0 + lane < a.T ? a.xs[t0 + lane] : 1.f;
+      constexpr int kStep = GATED ? 16 : 32;   // output features at a time
+      for (int c0 = h * (FT / 2); c0 < (h + 1) * (FT / 2); c0 += kStep) {
+        if (t0 >= a.T || n0 + c0 >= a.N) break;   // the same for the whole warp
+        uint32_t v[32];
+        if constexpr (GATED) {
+          uint32_t g[16], w[16];
+          tmem_ld16(d + (uint32_t)c0, g);
+          tmem_ld16(d + (uint32_t)(BN / 2 + c0), w);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            v[j] = g[j];
+            v[16 + j] = w[j];
+          }
+        } else {
+          tmem_ld32(d + (uint32_t)c0, v);
+          tmem_wait_ld();
+        }
+        if (a.xs) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * xs);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(buf + lane * 32 + ((j ^ (lane & 7)) * 4)) =
+              make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        __syncwarp();
+        finish_turned<GATED, O>(a, buf, t0, n0 + c0, lane);
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                         map_to_rank(&acc_empty[acc.i], 0))
+                     : "memory");
+      acc.next(2);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // nothing of the peer is still on its way here
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
+  }
 }
 
 // ------------------------------------------------------------ tensor maps
@@ -320,17 +765,16 @@ int split_of(int tiles, int nk, int slots) {
   return best;
 }
 
-template <bool F8, int NT>
+template <bool F8, bool GATED, int NT>
 cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
   using C = NarrowCfg<NT>;
-  const bool gated = p.a.act == MOE_W4A16_ACT_SWIGLU;
-  const int FT = gated ? 64 : 128;
+  constexpr int FT = GATED ? 64 : 128;
   CUtensorMap mw, mx;
-  if (!encode_rows(&mw, p.w, gated ? 2ll * p.a.N : p.a.N, p.a.K, p.elem, p.ld_w, FT) ||
+  if (!encode_rows(&mw, p.w, GATED ? 2ll * p.a.N : p.a.N, p.a.K, p.elem, p.ld_w, FT) ||
       !encode_rows(&mx, p.x, p.a.T, p.a.K, p.elem, p.ld_x, NT))
     return cudaErrorInvalidValue;
-  auto kernel = linear_narrow_kernel<F8, NT>;
-  cudaError_t e = opt_in_smem((const void*)kernel, C::kSmem);
+  auto kernel = linear_narrow_kernel<F8, GATED, NT>;
+  const cudaError_t e = opt_in_smem((const void*)kernel, C::kSmem);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)((p.a.N + FT - 1) / FT) * ((p.a.T + NT - 1) / NT);
   const int nk = (p.a.K + kChunk / p.elem - 1) / (kChunk / p.elem);
@@ -339,12 +783,71 @@ cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
   return launch_pdl(kernel, dim3((unsigned)(tiles * S)), dim3(C::kThreads), C::kSmem, st, S, p.a, mw, mx, p.out_dtype, S);
 }
 
+template <bool F8, bool GATED, int BN, typename O>
+cudaError_t launch_wide_o(const Problem& p, cudaStream_t st) {
+  using C = WideCfg<BN>;
+  CUtensorMap mw, mx;
+  if (!encode_rows(&mw, p.w, GATED ? 2ll * p.a.N : p.a.N, p.a.K, p.elem, p.ld_w, BN / 2) ||
+      !encode_rows(&mx, p.x, p.a.T, p.a.K, p.elem, p.ld_x, 128))
+    return cudaErrorInvalidValue;
+  auto kernel = linear_wide_kernel<F8, GATED, BN, O>;
+  const cudaError_t e = opt_in_smem((const void*)kernel, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int FT = GATED ? BN / 2 : BN;
+  const long long tiles = (long long)((p.a.T + 255) / 256) * ((p.a.N + FT - 1) / FT);
+  if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
+  const long long pairs = p.num_sms / 2;
+  return launch_pdl(kernel, dim3((unsigned)((tiles < pairs ? tiles : pairs) * 2)), dim3(C::kThreads), C::kSmem, st, 2,
+                    p.a, mw, mx);
+}
+
+template <bool F8, bool GATED, int BN>
+cudaError_t launch_wide(const Problem& p, cudaStream_t st) {
+  return p.out_dtype == MOE_W4A16_F16    ? launch_wide_o<F8, GATED, BN, __half>(p, st)
+         : p.out_dtype == MOE_W4A16_BF16 ? launch_wide_o<F8, GATED, BN, __nv_bfloat16>(p, st)
+                                         : launch_wide_o<F8, GATED, BN, float>(p, st);
+}
+
+// The tile width of the wide kernel: rounds of tiles over the SM pairs, times
+// a tile's time.  A K chunk takes a pair 0.29 us at 256 weight rows, 0.17 at
+// 128 and 0.14 at 64 (below 128 the warps that fetch and issue set the pace),
+// a launch and its last epilogue 2.6, 1.7 and 1.2 us: in units of 5 ns.
+// Measured at N = K = 2048 with 256 / 128 / 64 rows: T = 512 14.7 / 8.9 / 8.3
+// us, T = 1024 15.2 / 10.2 / 13.0, T = 4096 25.9 / 27.2 / 36.4.
+template <bool GATED>
+int wide_rows(const Problem& p) {
+  const long long nk = (p.a.K + kChunk / p.elem - 1) / (kChunk / p.elem), pairs = p.num_sms / 2;
+  const int rows[3] = {256, 128, 64}, chunk[3] = {58, 34, 28}, fixed[3] = {520, 340, 240};
+  int best = 0;
+  long long cost = -1;
+  for (int i = 0; i < 3; ++i) {
+    const int ft = GATED ? rows[i] / 2 : rows[i];
+    const long long tiles = (long long)((p.a.T + 255) / 256) * ((p.a.N + ft - 1) / ft);
+    const long long c = (tiles + pairs - 1) / pairs * nk * chunk[i] + fixed[i];
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = rows[i];
+    }
+  }
+  return best;
+}
+
+// Up to 64 tokens the narrow kernel (N = K = 2048: T = 64 5.5 us, the wide one
+// 7.1; with a 128-token tile T = 128 took it 10.7, the wide one 7.3).
+template <bool F8, bool GATED>
+cudaError_t launch_gated(const Problem& p, cudaStream_t st) {
+  if (p.a.T <= 16) return launch_narrow<F8, GATED, 16>(p, st);
+  if (p.a.T <= 32) return launch_narrow<F8, GATED, 32>(p, st);
+  if (p.a.T <= 64) return launch_narrow<F8, GATED, 64>(p, st);
+  const int rows = wide_rows<GATED>(p);
+  return rows == 256   ? launch_wide<F8, GATED, 256>(p, st)
+         : rows == 128 ? launch_wide<F8, GATED, 128>(p, st)
+                       : launch_wide<F8, GATED, 64>(p, st);
+}
+
 template <bool F8>
 cudaError_t launch_linear(const Problem& p, cudaStream_t st) {
-  if (p.a.T <= 16) return launch_narrow<F8, 16>(p, st);
-  if (p.a.T <= 32) return launch_narrow<F8, 32>(p, st);
-  if (p.a.T <= 64) return launch_narrow<F8, 64>(p, st);
-  return launch_narrow<F8, 128>(p, st);
+  return p.a.act == MOE_W4A16_ACT_SWIGLU ? launch_gated<F8, true>(p, st) : launch_gated<F8, false>(p, st);
 }
 
 int elem_size(int dtype) { return dtype == MOE_W4A16_E4M3 ? 1 : dtype == MOE_W4A16_F32 ? 4 : 2; }
@@ -421,9 +924,9 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linea
   p.a.N = c.n;
   p.a.K = c.k;
   p.a.act = c.act;
-  // FP32 accumulator; operand formats: kind::f16 0 = FP16, 1 = BF16; kind::f8f6f4 0 = E4M3; M = 128
+  // FP32 accumulator; operand formats: kind::f16 0 = FP16, 1 = BF16; kind::f8f6f4 0 = E4M3
   const uint32_t fmt = c.in_dtype == MOE_W4A16_BF16 ? 1u : 0u;
-  p.a.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((128u >> 4) << 24);
+  p.a.idesc = (1u << 4) | (fmt << 7) | (fmt << 10);
   const size_t vb = 4 * (size_t)os;
   p.a.vec = blk::aligned(out, vb) && ld_out % 4 == 0 && (!residual || (blk::aligned(residual, vb) && ld_res % 4 == 0)) ? 4 : 1;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

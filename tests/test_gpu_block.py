@@ -54,7 +54,8 @@ def check_norm(x, res, w, eps, outs):
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
 @pytest.mark.parametrize("T,H", [(1, 1), (3, 7), (1, 64), (5, 130), (2, 2048), (67, 2047), (33, 2052), (9, 4096),
-                                 (3, 8191), (2, 8200), (2, 12289), (3, 16384), (1000, 256)])
+                                 (3, 8191), (2, 8200), (9, 12289), (9, 16383), (3, 16384),
+                                 (1000, 256), (129, 72), (37, 40), (41, 9), (8, 1023)])
 def test_norm_shapes(T, H, dtype):
     x, res, w = rand((T, H), dtype, 1), rand((T, H), dtype, 2, 3.0), rand((H,), dtype, 3)
     for r, ww, quant in ((res, w, True), (None, w, True), (res, None, False), (None, None, False)):
@@ -78,6 +79,23 @@ def test_norm_strides_and_alignment(off):
     check_norm(x, res, w, 1e-6, outs)
     assert (guard[:, :off] == 7).all() and (guard[:, off + H:] == 7).all() and (s[:, H:] == 7).all()
     assert (q.float()[:, :off] == 0).all() and (q.float()[:, off + H:] == 0).all()
+
+
+@pytest.mark.parametrize("T,H", [(5000, 1024), (4003, 1030), (3000, 2056), (2501, 4097), (2600, 8192), (2440, 9001),
+                                 (2433, 16384)])
+def test_norm_many_rows(T, H):
+    """Enough rows for the streaming kernel, every row against the direct kernel's and some against the oracle."""
+    for dtype, r, quant in ((torch.float16, True, True), (torch.bfloat16, False, False)):
+        x, w = rand((T, H), dtype, 1), rand((H,), dtype, 3)
+        res = rand((T, H), dtype, 2) if r else None
+        outs = B.add_rmsnorm(x, res, w, quant=quant)
+        pick = [0, 1, 2, T // 2, T - 2, T - 1]
+        cut = lambda t: None if t is None else t[pick]   # noqa: E731
+        check_norm(x[pick], cut(res), w, 1e-6, [cut(o) for o in outs])
+        for i in range(0, T, 500):   # the direct kernel's rows: within the roundings of two summation orders
+            few = B.add_rmsnorm(x[i:i + 500], None if res is None else res[i:i + 500], w)[0]
+            d = (few.double() - outs[0][i:i + 500].double()).abs()
+            assert (d <= 2.5 * U[dtype] * few.double().abs() + 2 * TINY[dtype]).all()
 
 
 def test_norm_in_place_and_rows_independent_of_batch():

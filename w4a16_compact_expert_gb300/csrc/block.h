@@ -43,6 +43,22 @@ inline moe_w4a16_status launch_failed(const char* op, cudaError_t e) {
   return MOE_W4A16_ERR_CUDA;
 }
 
+// SM count of the current device, asked once per device.
+inline int current_sms() {
+  static int sms[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (!sms[dev]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) cudaGetLastError();
+    sms[dev] = n;
+  }
+  return sms[dev];
+}
+
 inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 }  // namespace blk

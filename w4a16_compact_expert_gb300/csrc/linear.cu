@@ -852,22 +852,6 @@ cudaError_t launch_linear(const Problem& p, cudaStream_t st) {
 
 int elem_size(int dtype) { return dtype == MOE_W4A16_E4M3 ? 1 : dtype == MOE_W4A16_F32 ? 4 : 2; }
 
-// SM count of the current device, asked once per device.
-int current_sms() {
-  static int sms[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-    cudaGetLastError();
-    return 0;
-  }
-  if (!sms[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) cudaGetLastError();
-    sms[dev] = n;
-  }
-  return sms[dev];
-}
-
 }  // namespace
 
 extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linear_config* cfg, int64_t T,
@@ -911,7 +895,7 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linea
   p.ld_w = ld_w * es;
   p.elem = es;
   p.out_dtype = c.out_dtype;
-  p.num_sms = current_sms();
+  p.num_sms = blk::current_sms();
   if (p.num_sms < 1) return blk::launch_failed(op, cudaErrorNoDevice);
   p.a.xs = x_scale;
   p.a.ws = w_scale;

@@ -170,6 +170,44 @@ def test_route_borders_closer_than_fp32(score):
         check_route(logits, bias, k, score=score, groups=groups, top_groups=top, group_rank=2)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,top", [(64, 8, 1, 1), (64, 8, 8, 4), (256, 8, 8, 4), (60, 6, 6, 3), (30, 5, 1, 1)])
+def test_route_a_few_close_borders(score, E, k, groups, top):
+    """Pairs and triples of choices (and of group values) that FP32 cannot order, at every place of the order."""
+    T = 96
+    g = torch.Generator().manual_seed(E + k + groups)
+    logits = torch.randn(T, E, generator=g)
+    l = logits[0].double()
+    sc = (torch.softmax(l, -1) if score == "softmax" else torch.sigmoid(l)).numpy()
+    per = E // groups
+    want = np.linspace(1.0, 2.0, E)                       # choices far apart ..
+    np.random.default_rng(E).shuffle(want)
+    order = np.argsort(-want)
+    for r in range(0, E - 2, 3):                          # .. except every second and third of the order
+        want[order[r + 1]] = want[order[r]]
+        if r % 2:
+            want[order[r + 2]] = want[order[r]]
+    if groups > 1:                                        # groups 1 and 2 hold the same two largest choices
+        a, b = np.argsort(-want[per:2 * per])[:2] + per, np.argsort(-want[2 * per:3 * per])[:2] + 2 * per
+        want[b] = want[a]
+    bias = torch.from_numpy((want - sc).astype(np.float32)).cuda()   # back to `want` within a rounding of FP32
+    logits[:] = logits[0]
+    logits[1::2] += torch.randn(T // 2, E, generator=g) * 1e-6       # and rows a little off it
+    check_route(logits.cuda(), bias, k, score=score, groups=groups, top_groups=top, group_rank=2 if per > 1 else 1)
+    check_route(logits.cuda(), bias, k, score=score, groups=groups, top_groups=top, group_rank=1, renormalize=True)
+
+
+def test_route_close_groups_without_a_bias():
+    """Group sums that FP32 cannot order: two groups hold the same logits but for the last bits."""
+    T, E = 64, 64
+    logits = rand((T, E), torch.float32, 51)
+    logits[:, 8:16] = logits[:, 0:8] * (1 + 2.0 ** -23)
+    logits[:, 16:24] = logits[:, 0:8].flip(1)
+    for score in ("softmax", "sigmoid"):
+        for top in (1, 2, 3):
+            check_route(logits, None, 4, score=score, groups=8, top_groups=top, group_rank=2)
+
+
 def test_route_ties_go_to_the_lower_index():
     logits = torch.zeros(7, 96, device="cuda")
     logits[1] = torch.arange(96, device="cuda") % 3

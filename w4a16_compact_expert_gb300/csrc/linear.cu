@@ -39,6 +39,28 @@ struct LinearArgs {
   int vec;           // 4: four neighbouring outputs can be read and written at once, else 1
 };
 
+// a / (1 + e^-a); the quotient is 0 where e^-a passes 2^126, as it should be.
+DEV_INLINE float silu(float a) { return __fdividef(a, 1.f + __expf(-a)); }
+
+// a Phi(a) with the normal distribution's Phi(-|a|) = erfc(|a| / sqrt 2) / 2 by
+// formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions
+// (|error| of erf 1.5e-7); taken from the tail's side, so that large negative
+// a keep their relative accuracy.
+DEV_INLINE float gelu(float a) {
+  const float z = fabsf(a) * 0.70710678f;
+  const float t = __fdividef(1.f, fmaf(0.3275911f, z, 1.f));
+  const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                           0.254829592f);
+  const float tail = 0.5f * p * __expf(-z * z);   // Phi(-|a|)
+  return a > 0.f ? fmaf(-a, tail, a) : a * tail;
+}
+
+// (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+DEV_INLINE float gelu_tanh(float a) {
+  const float u = 0.7978845608f * fmaf(0.044715f * a, a * a, a);
+  return __fdividef(a, 1.f + __expf(-2.f * u));
+}
+
 // The switch stands outside the values' loop: one branch per value kept a
 // thread's values from overlapping (a 256 x 256 tile's epilogue took 7.5 us).
 template <int N>
@@ -50,16 +72,15 @@ DEV_INLINE void activate(float (&v)[N], int act) {
       break;
     case MOE_W4A16_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * (1.f + erff(v[i] * 0.70710678f));
+      for (int i = 0; i < N; ++i) v[i] = gelu(v[i]);
       break;
     case MOE_W4A16_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        v[i] = 0.5f * v[i] * (1.f + tanhf(0.7978845608f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
+      for (int i = 0; i < N; ++i) v[i] = gelu_tanh(v[i]);
       break;
     case MOE_W4A16_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = v[i] / (1.f + __expf(-v[i]));
+      for (int i = 0; i < N; ++i) v[i] = silu(v[i]);
       break;
     default: break;
   }
@@ -230,7 +251,7 @@ DEV_INLINE void activate_quads(const LinearArgs& a, int n, int step, float (&g)[
   }
   if constexpr (GATED) {
 #pragma unroll
-    for (int i = 0; i < Q * 4; ++i) g[i] = __fdividef(g[i], 1.f + __expf(-g[i])) * u[i];
+    for (int i = 0; i < Q * 4; ++i) g[i] = silu(g[i]) * u[i];
   } else {
     activate(g, a.act);
   }

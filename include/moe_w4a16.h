@@ -162,6 +162,20 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_forward(moe_w4a16_handle* h, const void
                                    int32_t* sorted_pairs, int32_t* expert_offsets,
                                    moe_w4a16_stream_t stream);
 
+/* The layer's experts on routing that the caller gives (moe_w4a16_route_scored,
+ * or any other rule) instead of the handle's softmax router:
+ *   out = (RESIDUAL ? x : 0) + sum_{j=0..k-1} topk_w[t][j] y(topk_ids[t][j])
+ * with y as in moe_w4a16_forward and the ranks summed in j order in FP32.
+ *   topk_ids [T][k] int32, topk_w [T][k] FP32: device, k = the handle's top_k.
+ * Flags: RESIDUAL, FORCE_GEMV, FORCE_GEMM.  An absent expert contributes 0 and
+ * counts as a miss; an id outside [0, E) counts as a miss too and is taken as
+ * expert 0 with weight 0.  Runs as separate launches in every regime (1 or 3
+ * for the permutation, then the decode kernels or the grouped GEMM; see
+ * moe_w4a16_last_path); everything else as for moe_w4a16_forward. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_forward_routed(moe_w4a16_handle* h, const void* x, int32_t T,
+                                                        const int32_t* topk_ids, const float* topk_w,
+                                                        uint32_t flags, void* out, moe_w4a16_stream_t stream);
+
 /* Same layer with HOST activations: copies x_host (FP16 [T][H]) into a
  * handle-owned device buffer, runs moe_w4a16_forward, copies the result into
  * out_host (FP16 [T][H]) and synchronises `stream` before returning.  Host
@@ -268,6 +282,8 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_set_gemv_max_tokens(moe_w4a16_handle* h
  *   MOE_W4A16_PATH_GEMM          router + gather (T <= 8: 1 + 1; above: 1
  *                                kernel that also gathers the x rows) +
  *                                gate/up GEMM + down GEMM + combine
+ *                                moe_w4a16_forward_routed: 1 or 3 kernels in
+ *                                the router's place, then gather + ...
  *   MOE_W4A16_PATH_OFFLOAD       router + gather (as above) + per batch of
  *                                execution slots (expand + dense gate/up GEMM
  *                                + dense down GEMM) + combine

@@ -97,6 +97,10 @@ def test_null_configs_and_no_rows(lib):
     assert linear(lib, T=0, x=None, w=None, out=None) == F.OK
 
 
+def test_routed_forward_without_a_handle(lib):
+    assert lib.moe_w4a16_forward_routed(None, P, 1, P, P, 0, P, None) == F.ERR_INVALID_ARG
+
+
 def test_binding_refuses_wrong_tensors():
     x = torch.zeros(2, 64, dtype=torch.float16)
     for f in (lambda: B.add_rmsnorm(x), lambda: B.linear(x, x), lambda: B.route_scored(x, 2)):

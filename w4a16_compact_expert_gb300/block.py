@@ -152,3 +152,38 @@ def linear(x, w, *, bias=None, act: str = "none", residual=None, x_scale=None, w
 def status() -> int:
     """Synchronises and clears the status of the block operators: OK or ERR_TIMEOUT."""
     return _lib().moe_w4a16_block_status()
+
+
+class MoEBlock:
+    """The feed-forward half of a decoder block around one MoELayer:
+
+        s   = x + residual                       the residual stream
+        n   = rmsnorm(s) * norm_weight           (and n in E4M3 for an 8-bit shared expert)
+        ids, w = route_scored(n router_w^T)
+        out = sum_j w_j expert_ids_j(n) + shared(n),   shared(n) = down(silu(gate n) * (up n))
+
+    Returns (out, s); the next block adds them up.  layer: a MoELayer with
+    experts and slot table set.  router_w fp16 [E, H]; shared: None or
+    (gate_up, down) with gate_up [2 Is, H] in fp16, or in E4M3 with
+    shared_scale fp32 [2 Is], and down fp16 [H, Is].  route: the keyword
+    arguments of route_scored.  The layer's rule on streams (one stream per
+    handle, or ordered by events) is the block's."""
+
+    def __init__(self, layer, norm_weight, router_w, shared=None, shared_scale=None, eps: float = 1e-6, **route):
+        self.layer, self.norm_weight, self.router_w, self.eps, self.route = layer, norm_weight, router_w, eps, route
+        self.gate_up, self.down = shared if shared is not None else (None, None)
+        self.scale = shared_scale
+        self.quant = self.gate_up is not None and self.gate_up.dtype is _E4M3
+        if self.quant != (shared_scale is not None):
+            raise ValueError("shared_scale goes with an E4M3 gate_up")
+
+    def __call__(self, x, residual=None, stream=None):
+        n, s, q, qs = add_rmsnorm(x, residual, self.norm_weight, eps=self.eps, quant=self.quant, stream=stream)
+        logits = linear(n, self.router_w, out_dtype=_F32, stream=stream)
+        ids, w = route_scored(logits, self.layer.cfg.top_k, stream=stream, **self.route)
+        out = _empty(n.shape, n.dtype, n, stream)
+        self.layer.forward_routed(n, ids, w, out=out, stream=stream)
+        if self.gate_up is not None:
+            h = linear(q if self.quant else n, self.gate_up, act="swiglu", x_scale=qs, w_scale=self.scale, stream=stream)
+            linear(h, self.down, residual=out, out=out, stream=stream)
+        return out, x if s is None else s

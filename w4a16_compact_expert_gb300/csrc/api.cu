@@ -475,6 +475,61 @@ moe_w4a16_status moe_w4a16_forward(moe_w4a16_handle* h, const void* x, int32_t T
   return MOE_W4A16_OK;
 }
 
+moe_w4a16_status moe_w4a16_forward_routed(moe_w4a16_handle* h, const void* x, int32_t T, const int32_t* topk_ids,
+                                          const float* topk_w, uint32_t flags, void* out, moe_w4a16_stream_t stream) {
+  if (!h) return MOE_W4A16_ERR_INVALID_ARG;
+  if (T < 0 || T > h->cfg.max_tokens)
+    return fail(h, MOE_W4A16_ERR_INVALID_ARG, "T=" + std::to_string(T) + " outside [0, max_tokens]");
+  if (flags & ~(MOE_W4A16_RESIDUAL | MOE_W4A16_FORCE_GEMV | MOE_W4A16_FORCE_GEMM))
+    return fail(h, MOE_W4A16_ERR_INVALID_ARG, "forward_routed takes RESIDUAL, FORCE_GEMV and FORCE_GEMM only");
+  if ((flags & MOE_W4A16_FORCE_GEMV) && (flags & MOE_W4A16_FORCE_GEMM))
+    return fail(h, MOE_W4A16_ERR_INVALID_ARG, "FORCE_GEMV and FORCE_GEMM are exclusive");
+  if (T == 0) {
+    h->last_path = MOE_W4A16_PATH_NONE;
+    h->last_launches = 0;
+    return MOE_W4A16_OK;
+  }
+  if (!x || !topk_ids || !topk_w || !out)
+    return fail(h, MOE_W4A16_ERR_INVALID_ARG, "NULL x, topk_ids, topk_w or out");
+  if (x == out) return fail(h, MOE_W4A16_ERR_INVALID_ARG, "out must not alias x");
+  if (((uintptr_t)x | (uintptr_t)out) & 15u)
+    return fail(h, MOE_W4A16_ERR_INVALID_ARG, "x and out must be 16-byte aligned");
+  if (((uintptr_t)topk_ids | (uintptr_t)topk_w) & 3u)
+    return fail(h, MOE_W4A16_ERR_INVALID_ARG, "topk_ids and topk_w must be 4-byte aligned");
+  if (!h->table_set) return fail(h, MOE_W4A16_ERR_INVALID_ARG, "slot table not set");
+  const bool shapes = gemm_shapes_supported(h->cfg.hidden, h->cfg.inter);
+  if ((flags & MOE_W4A16_FORCE_GEMM) && !shapes)
+    return fail(h, MOE_W4A16_ERR_UNSUPPORTED, "grouped GEMM path not available");
+  DeviceGuard dg(h->cfg.device);
+  if (!dg.ok) return fail(h, MOE_W4A16_ERR_CUDA, "cudaSetDevice failed");
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  FwdCtx c;
+  memset(&c, 0, sizeof c);
+  fill_ctx(h, c);
+  c.x = static_cast<const __half*>(x);
+  c.T = T;
+  c.flags = flags;
+  c.out = static_cast<__half*>(out);
+  c.ksplit = 1;
+  const bool gemm = (flags & MOE_W4A16_FORCE_GEMM) ||
+                    (!(flags & MOE_W4A16_FORCE_GEMV) && T > h->gemv_max_tokens && shapes);
+  c.tile_tokens = gemm_tile_tokens(T, c.k, c.E);
+  int ma = c.E;
+  if ((long long)T * c.k < ma) ma = T * c.k;
+  if (h->cfg.num_slots < ma) ma = h->cfg.num_slots;
+  c.max_active = ma;
+  cudaError_t e = record_stage(h->events, 0, st);
+  if (e == cudaSuccess) e = launch_route_given(c, topk_ids, topk_w, st);
+  if (e == cudaSuccess && !gemm) e = record_stage(h->events, 1, st);   // the GEMM family records it after the gather
+  if (e == cudaSuccess)
+    e = gemm ? launch_gemm_experts(c, h->maps, /*gathered=*/false, st, h->events) : launch_gemv_experts(c, st, h->events);
+  if (e == cudaErrorNotSupported) return fail(h, MOE_W4A16_ERR_UNSUPPORTED, "grouped GEMM path not available");
+  if (e != cudaSuccess) return cuda_fail(h, e, "expert launch");
+  h->last_path = gemm ? MOE_W4A16_PATH_GEMM : MOE_W4A16_PATH_DECODE;
+  h->last_launches = route_given_launches(c) + (gemm ? 4 : 2);
+  return MOE_W4A16_OK;
+}
+
 int32_t moe_w4a16_last_path(const moe_w4a16_handle* h, int32_t* launches) {
   if (!h) return -1;
   if (launches) *launches = h->last_launches;

@@ -139,6 +139,11 @@ cudaError_t launch_offload_experts(const FwdCtx& c, const DenseMaps& dm, bool ga
 // copy of the routed x rows into sorted-row order (c.xp).
 cudaError_t launch_route_gather(const FwdCtx& c, bool gather, cudaStream_t st);
 
+// route.cu: routing given by the caller (ids and weights [T*k]) instead of the
+// router: copied, checked and permuted in 1 or 3 launches.
+cudaError_t launch_route_given(const FwdCtx& c, const int32_t* ids, const float* w, cudaStream_t st);
+int route_given_launches(const FwdCtx& c);
+
 // route: the largest T handled by the single-launch cluster router (its
 // 8 CTAs take about 4 us per 8 tokens; the cooperative router is faster above)
 #define ROUTE_FUSED_MAX_T 8

@@ -673,6 +673,49 @@ __global__ void __launch_bounds__(256) route_coop_kernel(FwdCtx c) {
   }
 }
 
+// ------------------------------------------------- routing given by the caller
+// Copies the caller's ids and weights into the handle's routing buffers.  An id
+// outside [0, E) becomes expert 0 with weight 0 and counts as a miss, so that
+// no index leaves its array.
+DEV_INLINE int take_given(const FwdCtx& c, const int32_t* ids, const float* w, int p) {
+  int e = ids[p];
+  float v = w[p];
+  if ((unsigned)e >= (unsigned)c.E) {
+    e = 0;
+    v = 0.f;
+    atomicAdd(&c.status->miss, 1ull);
+    atomicOr(&c.status->flags, STATUS_MISS);
+  }
+  c.ids[p] = e;
+  c.topw[p] = v;
+  return e;
+}
+
+// Few pairs: one CTA copies and permutes.
+__global__ void __launch_bounds__(256) route_given_small_kernel(FwdCtx c, const int32_t* ids, const float* w) {
+  extern __shared__ int psm[];
+  pdl_wait();
+  pdl_trigger();
+  for (int p = threadIdx.x; p < c.T * c.k; p += blockDim.x) take_given(c, ids, w, p);
+  __syncthreads();   // the ids (global) are visible to the whole CTA
+  permute_block(c, c.ids, psm);
+}
+
+// Many: one CTA per 8-token block copies and counts its pairs per expert
+// (route_hist row = blockIdx.x); the scan and the scatter follow as after the
+// logits router.
+__global__ void __launch_bounds__(256) route_given_kernel(FwdCtx c, const int32_t* ids, const float* w) {
+  __shared__ int hcount[256];
+  pdl_wait();
+  pdl_trigger();
+  for (int e = threadIdx.x; e < c.E; e += blockDim.x) hcount[e] = 0;
+  __syncthreads();
+  const int p0 = blockIdx.x * 8 * c.k, p1 = min(c.T, (int)blockIdx.x * 8 + 8) * c.k;
+  for (int p = p0 + (int)threadIdx.x; p < p1; p += blockDim.x) atomicAdd(&hcount[take_given(c, ids, w, p)], 1);   // order-free
+  __syncthreads();
+  for (int e = threadIdx.x; e < c.E; e += blockDim.x) c.route_hist[(size_t)blockIdx.x * c.E + e] = hcount[e];
+}
+
 }  // namespace
 
 bool route_single_launch(const FwdCtx& c) { return route_cluster_smem(c.T, c.E, c.H, c.k) <= 200 * 1024; }
@@ -730,4 +773,20 @@ cudaError_t launch_route_gather(const FwdCtx& c, bool gather, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, route_coop_kernel<false>, cc);
+}
+
+// One CTA takes up to this many pairs (512 pairs: 5 us, the three launches 7).
+constexpr int kGivenSmallPairs = 1024;
+
+int route_given_launches(const FwdCtx& c) { return c.T * c.k <= kGivenSmallPairs ? 1 : 3; }
+
+cudaError_t launch_route_given(const FwdCtx& c, const int32_t* ids, const float* w, cudaStream_t st) {
+  if (route_given_launches(c) == 1) {
+    const size_t smem = ((size_t)8 * c.E + 2 * c.E + 1) * sizeof(int);
+    return launch_pdl(route_given_small_kernel, dim3(1), dim3(256), smem, st, 1, c, ids, w);
+  }
+  cudaError_t e = launch_pdl(route_given_kernel, dim3((c.T + 7) / 8), dim3(256), 0, st, 1, c, ids, w);
+  if (e == cudaSuccess) e = launch_pdl(route_scan_kernel, dim3(c.E), dim3(256), 0, st, 1, c);
+  if (e == cudaSuccess) e = launch_pdl(route_scatter_kernel, dim3((c.T + 7) / 8), dim3(256), 0, st, 1, c);
+  return e;
 }

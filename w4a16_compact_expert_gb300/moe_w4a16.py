@@ -28,7 +28,7 @@ EXPORTED = ["moe_w4a16_create", "moe_w4a16_destroy", "moe_w4a16_pack_experts", "
             "moe_w4a16_cache_release", "moe_w4a16_cache_get_stats", "moe_w4a16_cache_slot_of",
             "moe_w4a16_cache_last_error", "moe_w4a16_cache_create_sim", "moe_w4a16_cache_sim_complete",
             "moe_w4a16_cache_sim_fail", "moe_w4a16_selftest_timeout", "moe_w4a16_offload_enable", "moe_w4a16_add_rmsnorm",
-            "moe_w4a16_route_scored", "moe_w4a16_linear", "moe_w4a16_block_status"]
+            "moe_w4a16_route_scored", "moe_w4a16_linear", "moe_w4a16_block_status", "moe_w4a16_forward_routed"]
 PATH_NONE, PATH_DECODE_FUSED, PATH_DECODE, PATH_GEMM, PATH_OFFLOAD = 0, 1, 2, 3, 4
 PATH_NAMES = {PATH_NONE: "none", PATH_DECODE_FUSED: "decode_fused", PATH_DECODE: "decode", PATH_GEMM: "gemm",
               PATH_OFFLOAD: "offload_qpacked"}
@@ -78,6 +78,7 @@ def load_library(path: str = LIB_PATH):
     lib.moe_w4a16_pack_experts.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, vp, vp]
     lib.moe_w4a16_set_slot_table.argtypes = [vp, vp, vp]
     lib.moe_w4a16_forward.argtypes = [vp, vp, i32, vp, vp, u32, vp, vp, vp, vp, vp, vp]
+    lib.moe_w4a16_forward_routed.argtypes = [vp, vp, i32, vp, vp, u32, vp, vp]
     lib.moe_w4a16_forward_host.argtypes = [vp, vp, i32, vp, vp, u32, vp, vp]
     lib.moe_w4a16_forward_host_async.argtypes = [vp, vp, i32, vp, vp, u32, vp, vp]
     lib.moe_w4a16_get_status.argtypes = [vp, i64p]
@@ -219,6 +220,21 @@ class MoELayer:
             self.h, _ptr(x), T, _ptr(router_w), _ptr(bias), flags, _ptr(out), _ptr(dbg.get("ids")),
             _ptr(dbg.get("weights")), _ptr(dbg.get("sorted_pairs")), _ptr(dbg.get("offsets")), _stream(stream)))
         return (out, dbg) if debug else out
+
+    def forward_routed(self, x, ids, weights, flags: int = 0, out=None, stream=None):
+        """The experts on given routing: x cuda fp16 [T, H], ids int32 and weights fp32 [T, top_k]."""
+        import torch
+        T = int(x.shape[0])
+        if ids.dtype != torch.int32 or weights.dtype != torch.float32 or ids.shape != (T, self.cfg.top_k) or \
+                weights.shape != ids.shape:
+            raise ValueError(f"ids (int32) and weights (float32) must have shape ({T}, {self.cfg.top_k})")
+        if x.dtype != torch.float16 or x.dim() != 2 or x.shape[1] != self.cfg.hidden:
+            raise ValueError(f"x must be float16 of shape (T, {self.cfg.hidden})")
+        if out is None:
+            out = torch.empty_like(x)
+        self._check(self.lib.moe_w4a16_forward_routed(self.h, _ptr(x), T, _ptr(ids), _ptr(weights), flags, _ptr(out),
+                                                      _stream(stream)))
+        return out
 
     def forward_raw(self, x_ptr: int, T: int, router_w_ptr: int, bias_ptr, flags: int, out_ptr: int, stream_ptr):
         """Pointer-level forward (no torch objects), for timing loops."""

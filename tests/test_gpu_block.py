@@ -315,6 +315,16 @@ def test_linear_every_pipeline_stage(T, act, N, K):
         check_linear(*t, act, B.linear(x, w, act=act, x_scale=xs, w_scale=ws, out_dtype=F16))
 
 
+@pytest.mark.parametrize("T,N,K,act", [(1100, 9000, 208, "none"), (1100, 9000, 256, "gelu"), (2000, 4100, 144, "swiglu"),
+                                       (1500, 4097, 512, "swiglu"), (260, 20000, 176, "none"), (4000, 300, 1040, "silu")])
+def test_linear_wide_many_tiles(T, N, K, act):
+    """More tiles than resident CTAs, rows on and off 128-byte lines, every output."""
+    for dtype in (F16, E4):
+        t = make_linear(T, N, K, dtype, act, True, False, F16, T)
+        x, w, xs, ws, b, _ = t
+        check_linear(*t, act, B.linear(x, w, act=act, bias=b, x_scale=xs, w_scale=ws, out_dtype=F16))
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 100, 16), (5, 64, 2048), (40, 129, 272), (130, 300, 1024)])
 @pytest.mark.parametrize("out", [F16, BF16, F32], ids=["fp16", "bf16", "fp32"])
 @pytest.mark.parametrize("act", ["none", "swiglu"])
@@ -369,6 +379,11 @@ def test_linear_masked_and_nonfinite_values():
     assert torch.isnan(out[2]).all() and not torch.isfinite(out[1]).any()
     check_linear(x[[0, 3]], w, None, None, None, None, "none", out[[0, 3]])
     assert torch.isnan(B.linear(x, w, act="relu")[2]).all()
+    one = torch.ones(1, 8, dtype=F16, device="cuda")
+    big = torch.tensor([[6e4, 0, 0, 0, 0, 0, 0, 0]] * 2, device="cuda").half() * torch.tensor([[1.0], [-1.0]], device="cuda").half()
+    for act in ("gelu", "gelu_tanh", "silu"):   # far out the activations are a and 0, not NaN
+        got = B.linear(one, big, act=act, out_dtype=F32)[0]
+        assert got[0] == big[0, 0].float() and got[1].abs() < 1e-3, act
 
 
 def test_linear_no_rows():

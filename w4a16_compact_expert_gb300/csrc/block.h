@@ -44,7 +44,7 @@ inline moe_w4a16_status launch_failed(const char* op, cudaError_t e) {
 }
 
 // SM count of the current device, asked once per device.
-inline int current_sms() {
+inline int current_sms(int* device = nullptr) {
   static int sms[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
@@ -56,6 +56,7 @@ inline int current_sms() {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) cudaGetLastError();
     sms[dev] = n;
   }
+  if (device) *device = dev;
   return sms[dev];
 }
 

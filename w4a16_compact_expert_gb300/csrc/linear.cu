@@ -19,6 +19,7 @@
 // tile's epilogue runs under the next tile's MMAs.
 // T = 2048, W [11264][2048]: E4M3 37 us (2,550 TFLOP/s), FP16 56 us (1,690).
 #include <cuda.h>
+#include <atomic>
 
 #include "block.h"
 
@@ -52,7 +53,7 @@ DEV_INLINE float gelu(float a) {
   const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
                            0.254829592f);
   const float tail = 0.5f * p * __expf(-z * z);   // Phi(-|a|)
-  return a > 0.f ? fmaf(-a, tail, a) : a * tail;
+  return a * (a > 0.f ? 1.f - tail : tail);
 }
 
 // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
@@ -113,7 +114,7 @@ DEV_INLINE void umma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t
 }
 
 // Arrives on `bar` once the MMAs issued so far are done; the pair form at its
-// place in both CTAs.
+// place in every CTA of the mask.
 DEV_INLINE void commit_one(uint64_t* bar, uint32_t leader) {
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
@@ -121,12 +122,12 @@ DEV_INLINE void commit_one(uint64_t* bar, uint32_t leader) {
       "r"(leader)
       : "memory");
 }
-DEV_INLINE void commit_pair(uint64_t* bar, uint32_t leader) {
+DEV_INLINE void commit_pair(uint64_t* bar, uint32_t mask, uint32_t leader) {
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
       " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3), "r"(leader)
+      "h"((uint16_t)mask), "r"(leader)
       : "memory");
 }
 
@@ -156,6 +157,18 @@ DEV_INLINE void fetch(uint32_t dst, const CUtensorMap* tmap, int c0, int r0, uin
         " [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
         "l"(tmap), "r"(c0), "r"(r0), "r"(bar), "r"(leader)
         : "memory");
+}
+
+// TMA box -> the same place in every CTA of the mask; each counts it at the
+// barrier of its pair's first CTA (`bar` is the address in such a CTA).
+DEV_INLINE void fetch_shared(uint32_t dst, const CUtensorMap* tmap, int c0, int r0, uint32_t bar, uint32_t mask,
+                             uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %6, 0;\n"
+      " @q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+      ".cta_group::2 [%0], [%1, {%2, %3}], [%4], %5;\n}\n" ::"r"(dst),
+      "l"(tmap), "r"(c0), "r"(r0), "r"(bar), "h"((uint16_t)mask), "r"(leader)
+      : "memory");
 }
 
 // Starts a box on its way into the L2 cache.  Allowed before the grids ahead
@@ -508,7 +521,11 @@ __global__ void __launch_bounds__(192, 2)
 // -------------------------------------------------------------------- wide
 // A pair of CTAs shares one tile of 256 tokens x BN weight rows: each loads
 // its 128 token rows and half of the weight rows, the first issues the MMAs of
-// both, and each finishes its 128 tokens.
+// both, and each finishes its 128 tokens.  PAIRS = 2: two pairs with
+// neighbouring weight tiles form a cluster and share their token rows: each CTA
+// loads half of its 128 rows for itself and its counterpart (TMA multicast).
+// That saves a quarter of a 256-row tile's reads from the L2, a third of a
+// 128-row tile's.
 template <int BN>
 struct WideCfg {
   static constexpr int kA = 128 * kChunk;   // the 128 token rows of this CTA
@@ -574,7 +591,7 @@ DEV_INLINE void finish_turned(const LinearArgs& a, const float* buf, int t0, int
   store_quads<O, kPass>(a, t, live, n0 + c, step, v);
 }
 
-template <bool F8, bool GATED, int BN, typename O>
+template <bool F8, bool GATED, int BN, int PAIRS, typename O>
 __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     linear_wide_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmX) {
@@ -591,11 +608,14 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
   uint64_t* acc_empty = acc_full + 2;        // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)cluster_rank();
+  const int crank = (int)cluster_rank(), rank = crank & 1, pair = crank >> 1;   // rank: in the pair
   const int mtiles = (a.T + 255) / 256;
-  const int tiles = mtiles * ((a.N + FT - 1) / FT);
+  // a unit of work: the tile of each of the cluster's pairs; with an odd number
+  // of weight tiles the last unit's second tile is empty (zeros, not stored)
+  const int tiles = mtiles * ((a.N + FT * PAIRS - 1) / (FT * PAIRS));
   const int nk = (a.K + kElem - 1) / kElem;
-  const int first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int first = blockIdx.x / (2 * PAIRS), step = gridDim.x / (2 * PAIRS);
+  const uint32_t pair_mask = 3u << (crank & ~1), all_mask = (1u << (2 * PAIRS)) - 1u;
 
   if (threadIdx.x == 32) {
     prefetch_map(&tmW);
@@ -604,7 +624,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], PAIRS);   // every pair that reads this CTA's loads
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&acc_full[s], 1);
@@ -630,9 +650,9 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     Pipe p;
     bool ok = true;
     int issued = 0;
-    const uint32_t leader = elect_lane(), ring = smem_u32(smem), bars = smem_u32(full), bars0 = map_to_rank(full, 0);
+    const uint32_t leader = elect_lane(), ring = smem_u32(smem), bars = smem_u32(full), bars0 = map_to_rank(full, crank & ~1);
     for (int tile = first; tile < tiles && ok; tile += step) {
-      const int m0 = (tile % mtiles) * 256 + rank * 128, n0 = (tile / mtiles) * FT;
+      const int m0 = (tile % mtiles) * 256 + rank * 128, n0 = (tile / mtiles * PAIRS + pair) * FT;
       const int b0 = rank == 0 ? n0 : GATED ? a.N + n0 : n0 + BN / 2;   // this CTA's weight rows
       for (int k = 0; k < nk; ++k) {
         if (!mbar_wait_bounded(&empty[p.i], p.ph ^ 1u, &g_block_status)) {
@@ -641,7 +661,10 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
         }
         const uint32_t dst = ring + (uint32_t)(p.i * C::kStage), bar0 = bars0 + (uint32_t)(p.i * 8);
         if (rank == 0) expect_bytes(bars + (uint32_t)(p.i * 8), (uint32_t)(2 * C::kStage), leader);
-        fetch<2>(dst, &tmX, k * kElem, m0, bar0, leader);
+        if constexpr (PAIRS == 1)
+          fetch<2>(dst, &tmX, k * kElem, m0, bar0, leader);
+        else   // rows 64 pair .. + 63 of the 128, for both pairs' CTAs of this rank
+          fetch_shared(dst + pair * (C::kA / 2), &tmX, k * kElem, m0 + pair * 64, bar0, 5u << rank, leader);
         fetch<2>(dst + C::kA, &tmW, k * kElem, b0, bar0, leader);
         ++issued;
         p.next(C::kStages);
@@ -676,10 +699,10 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             umma<F8, 2>(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (uint32_t)((k | j) != 0), leader);
-          commit_pair(&empty[p.i], leader);
+          commit_pair(&empty[p.i], all_mask, leader);
           p.next(C::kStages);
         }
-        if (ok) commit_pair(&acc_full[acc.i], leader);
+        if (ok) commit_pair(&acc_full[acc.i], pair_mask, leader);
         acc.next(2);
       }
     }
@@ -693,7 +716,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     for (int tile = first; tile < tiles; tile += step) {
       if (!mbar_wait_bounded(&acc_full[acc.i], acc.ph, &g_block_status)) break;
       tc_fence_after();
-      const int t0 = (tile % mtiles) * 256 + rank * 128 + q * 32, n0 = (tile / mtiles) * FT;
+      const int t0 = (tile % mtiles) * 256 + rank * 128 + q * 32, n0 = (tile / mtiles * PAIRS + pair) * FT;
       const uint32_t d = tmem + (uint32_t)(acc.i * BN) + ((uint32_t)(q * 32) << 16);
       const float xs = a.xs && t0 + lane < a.T ? a.xs[t0 + lane] : 1.f;
       constexpr int kStep = GATED ? 16 : 32;   // output features at a time
@@ -730,7 +753,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
       __syncwarp();
       if (lane == 0)
         asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                         map_to_rank(&acc_empty[acc.i], 0))
+                         map_to_rank(&acc_empty[acc.i], crank & ~1))
                      : "memory");
       acc.next(2);
     }
@@ -783,17 +806,37 @@ struct Problem {
   LinearArgs a;
   const void *x, *w;
   int64_t ld_x, ld_w;   // bytes
-  int elem, out_dtype, num_sms;
+  int elem, out_dtype, num_sms, dev;
 };
 
-// CTAs of a cluster share a tile's K chunks.  The split that ends first, with
-// `slots` CTAs at a time and each costing its chunks and about four chunks'
-// time for its start, its share of the sum and its stores.
-int split_of(int tiles, int nk, int slots) {
+constexpr int kMaxDevices = 64;
+
+// Clusters of a kernel that can be resident at once.  GPCs hold a whole number
+// of clusters: at one CTA per SM 76 of 2 but 36 of 4, at two 152 of 2, 97 of 3,
+// 74 of 4, 36 of 8.
+cudaError_t active_clusters(const void* kernel, int threads, size_t smem, int cluster, int* n) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cluster);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+  return e == cudaSuccess && *n < 1 ? cudaErrorLaunchOutOfResources : e;
+}
+
+// CTAs of a cluster share a tile's K chunks.  The split that ends first, each
+// CTA costing its chunks and about four chunks' time for its start, its share
+// of the sum and its stores.
+int split_of(int tiles, int nk, const int (&slots)[9]) {
   int best = 1;
   long long cost = -1;
   for (int s = 1; s <= 8 && s <= nk; ++s) {
-    const long long waves = ((long long)tiles * s + slots - 1) / slots;
+    const long long waves = (tiles + slots[s] - 1) / slots[s];   // slots[s] clusters of s at a time
     const long long c = waves * ((nk + s - 1) / s + 4);
     if (cost < 0 || c < cost) {
       cost = c;
@@ -816,7 +859,17 @@ cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)((p.a.N + FT - 1) / FT) * ((p.a.T + NT - 1) / NT);
   const int nk = (p.a.K + kChunk / p.elem - 1) / (kChunk / p.elem);
-  const int S = tiles > (1 << 24) ? 1 : split_of((int)tiles, nk, 2 * p.num_sms);
+  static std::atomic<int> resident[kMaxDevices][9];   // clusters of s CTAs that run at once, asked once per device
+  int slots[9];
+  for (int s = 1; s <= 8; ++s) {
+    slots[s] = resident[p.dev][s].load(std::memory_order_relaxed);
+    if (!slots[s]) {
+      const cudaError_t q = active_clusters((const void*)kernel, C::kThreads, C::kSmem, s, &slots[s]);
+      if (q != cudaSuccess) return q;
+      resident[p.dev][s].store(slots[s], std::memory_order_relaxed);
+    }
+  }
+  const int S = tiles > (1 << 24) ? 1 : split_of((int)tiles, nk, slots);
   if (tiles * S > 0x7fffffff) return cudaErrorInvalidConfiguration;
   // Grids of more CTAs than SMs keep the memory busy to their end, and the next
   // grid's prefetch takes over there (W [11264][2048] FP16 9.8 -> 9.3 us);
@@ -826,53 +879,68 @@ cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
                     prefetch);
 }
 
-template <bool F8, bool GATED, int BN, typename O>
+template <bool F8, bool GATED, int BN, int PAIRS, typename O>
 cudaError_t launch_wide_o(const Problem& p, cudaStream_t st) {
   using C = WideCfg<BN>;
   CUtensorMap mw, mx;
   if (!encode_rows(&mw, p.w, GATED ? 2ll * p.a.N : p.a.N, p.a.K, p.elem, p.ld_w, BN / 2) ||
-      !encode_rows(&mx, p.x, p.a.T, p.a.K, p.elem, p.ld_x, 128))
+      !encode_rows(&mx, p.x, p.a.T, p.a.K, p.elem, p.ld_x, 128 / PAIRS))
     return cudaErrorInvalidValue;
-  auto kernel = linear_wide_kernel<F8, GATED, BN, O>;
-  const cudaError_t e = opt_in_smem((const void*)kernel, C::kSmem);
+  auto kernel = linear_wide_kernel<F8, GATED, BN, PAIRS, O>;
+  cudaError_t e = opt_in_smem((const void*)kernel, C::kSmem);
   if (e != cudaSuccess) return e;
-  const int FT = GATED ? BN / 2 : BN;
-  const long long tiles = (long long)((p.a.T + 255) / 256) * ((p.a.N + FT - 1) / FT);
-  if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
-  const long long pairs = p.num_sms / 2;
-  return launch_pdl(kernel, dim3((unsigned)((tiles < pairs ? tiles : pairs) * 2)), dim3(C::kThreads), C::kSmem, st, 2,
-                    p.a, mw, mx);
+  static std::atomic<int> resident[kMaxDevices];   // clusters that run at once, asked once per device
+  int n = resident[p.dev].load(std::memory_order_relaxed);
+  if (!n) {
+    e = active_clusters((const void*)kernel, C::kThreads, C::kSmem, 2 * PAIRS, &n);
+    if (e != cudaSuccess) return e;
+    resident[p.dev].store(n, std::memory_order_relaxed);
+  }
+  const int FT = (GATED ? BN / 2 : BN) * PAIRS;
+  const long long units = (long long)((p.a.T + 255) / 256) * ((p.a.N + FT - 1) / FT);
+  if (units > 0x1fffffff) return cudaErrorInvalidConfiguration;
+  return launch_pdl(kernel, dim3((unsigned)((units < n ? units : n) * 2 * PAIRS)), dim3(C::kThreads), C::kSmem, st,
+                    2 * PAIRS, p.a, mw, mx);
 }
 
-template <bool F8, bool GATED, int BN>
+template <bool F8, bool GATED, int BN, int PAIRS>
 cudaError_t launch_wide(const Problem& p, cudaStream_t st) {
-  return p.out_dtype == MOE_W4A16_F16    ? launch_wide_o<F8, GATED, BN, __half>(p, st)
-         : p.out_dtype == MOE_W4A16_BF16 ? launch_wide_o<F8, GATED, BN, __nv_bfloat16>(p, st)
-                                         : launch_wide_o<F8, GATED, BN, float>(p, st);
+  return p.out_dtype == MOE_W4A16_F16    ? launch_wide_o<F8, GATED, BN, PAIRS, __half>(p, st)
+         : p.out_dtype == MOE_W4A16_BF16 ? launch_wide_o<F8, GATED, BN, PAIRS, __nv_bfloat16>(p, st)
+                                         : launch_wide_o<F8, GATED, BN, PAIRS, float>(p, st);
 }
 
-// The tile width of the wide kernel: rounds of tiles over the SM pairs, times
-// a tile's time.  A K chunk takes a pair 0.29 us at 256 weight rows, 0.17 at
-// 128 and 0.14 at 64 (below 128 the warps that fetch and issue set the pace),
-// a launch and its last epilogue 2.6, 1.7 and 1.2 us: in units of 5 ns.
-// Measured at N = K = 2048 with 256 / 128 / 64 rows: T = 512 14.7 / 8.9 / 8.3
-// us, T = 1024 15.2 / 10.2 / 13.0, T = 4096 25.9 / 27.2 / 36.4.
+// The tile width of the wide kernel: rounds of tiles over the resident
+// clusters, times a tile's time.  A K chunk takes a pair 0.29 us at 256 weight
+// rows, 0.17 at 128 and 0.14 at 64 (below 128 the warps that fetch and issue
+// set the pace), a launch and its last epilogue 2.6, 1.7 and 1.2 us: in units
+// of 5 ns.  Measured at N = K = 2048 with 256 / 128 / 64 rows: T = 512 14.2 /
+// 9.0 / 8.2 us, T = 1024 14.5 / 10.1 / 12.8, T = 4096 24.6 / 26.3 / 36.0.
 template <bool GATED>
-int wide_rows(const Problem& p) {
-  const long long nk = (p.a.K + kChunk / p.elem - 1) / (kChunk / p.elem), pairs = p.num_sms / 2;
+int wide_rows(const Problem& p, int pairs) {
+  const long long nk = (p.a.K + kChunk / p.elem - 1) / (kChunk / p.elem);
+  const long long slots = pairs == 1 ? p.num_sms / 2 : p.num_sms * 9 / 38;   // of 152 SMs: 76 pairs, 36 clusters of two
   const int rows[3] = {256, 128, 64}, chunk[3] = {58, 34, 28}, fixed[3] = {520, 340, 240};
   int best = 0;
   long long cost = -1;
   for (int i = 0; i < 3; ++i) {
-    const int ft = GATED ? rows[i] / 2 : rows[i];
-    const long long tiles = (long long)((p.a.T + 255) / 256) * ((p.a.N + ft - 1) / ft);
-    const long long c = (tiles + pairs - 1) / pairs * nk * chunk[i] + fixed[i];
+    const int ft = (GATED ? rows[i] / 2 : rows[i]) * pairs;
+    const long long units = (long long)((p.a.T + 255) / 256) * ((p.a.N + ft - 1) / ft);
+    const long long c = (units + slots - 1) / slots * nk * chunk[i] + fixed[i];
     if (cost < 0 || c < cost) {
       cost = c;
       best = rows[i];
     }
   }
   return best;
+}
+
+template <bool F8, bool GATED, int PAIRS>
+cudaError_t launch_wide_rows(const Problem& p, cudaStream_t st) {
+  const int rows = wide_rows<GATED>(p, PAIRS);
+  return rows == 256   ? launch_wide<F8, GATED, 256, PAIRS>(p, st)
+         : rows == 128 ? launch_wide<F8, GATED, 128, PAIRS>(p, st)
+                       : launch_wide<F8, GATED, 64, PAIRS>(p, st);
 }
 
 // Up to 64 tokens the narrow kernel (N = K = 2048: T = 64 5.5 us, the wide one
@@ -882,10 +950,13 @@ cudaError_t launch_gated(const Problem& p, cudaStream_t st) {
   if (p.a.T <= 16) return launch_narrow<F8, GATED, 16>(p, st);
   if (p.a.T <= 32) return launch_narrow<F8, GATED, 32>(p, st);
   if (p.a.T <= 64) return launch_narrow<F8, GATED, 64>(p, st);
-  const int rows = wide_rows<GATED>(p);
-  return rows == 256   ? launch_wide<F8, GATED, 256>(p, st)
-         : rows == 128 ? launch_wide<F8, GATED, 128>(p, st)
-                       : launch_wide<F8, GATED, 64>(p, st);
+  // Two pairs to a cluster where rows do not start on 128-byte lines: each box
+  // row then touches two lines and up to five sectors, the L2 sets the pace,
+  // and sharing the tokens helps (K = 1416, N = 4000 FP16: T = 333 12.0 -> 9.0
+  // us, T = 4096 42.6 -> 35.1).  On lines it does not (K = 2048, N = 2048, T =
+  // 4096 24.6 and 24.6), and fewer SMs fit the larger clusters.
+  const bool lines = p.ld_x % 128 == 0 && p.ld_w % 128 == 0;
+  return lines ? launch_wide_rows<F8, GATED, 1>(p, st) : launch_wide_rows<F8, GATED, 2>(p, st);
 }
 
 template <bool F8>
@@ -938,7 +1009,7 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linea
   p.ld_w = ld_w * es;
   p.elem = es;
   p.out_dtype = c.out_dtype;
-  p.num_sms = blk::current_sms();
+  p.num_sms = blk::current_sms(&p.dev);
   if (p.num_sms < 1) return blk::launch_failed(op, cudaErrorNoDevice);
   p.a.xs = x_scale;
   p.a.ws = w_scale;

@@ -811,10 +811,18 @@ struct Problem {
 
 constexpr int kMaxDevices = 64;
 
-// Clusters of a kernel that can be resident at once.  GPCs hold a whole number
-// of clusters: at one CTA per SM 76 of 2 but 36 of 4, at two 152 of 2, 97 of 3,
-// 74 of 4, 36 of 8.
-cudaError_t active_clusters(const void* kernel, int threads, size_t smem, int cluster, int* n) {
+// Asked about below in the place of the kernels of its shape, never launched:
+// for a kernel that allocates tensor memory the occupancy query answers one
+// CTA per SM, whatever it allocates.
+__global__ void __launch_bounds__(320) shape_kernel() {}
+
+// Clusters of CTAs of this shape that can be resident at once.  GPCs hold a
+// whole number of clusters: at one CTA per SM 76 of 2 but 36 of 4, at two 152 of
+// 2, 97 of 3, 74 of 4, 36 of 8.
+cudaError_t active_clusters(int threads, size_t smem, int cluster, int* n) {
+  const void* kernel = (const void*)shape_kernel;
+  cudaError_t e = opt_in_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cluster);
   cfg.blockDim = dim3((unsigned)threads);
@@ -825,19 +833,22 @@ cudaError_t active_clusters(const void* kernel, int threads, size_t smem, int cl
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+  e = cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
   return e == cudaSuccess && *n < 1 ? cudaErrorLaunchOutOfResources : e;
 }
 
 // CTAs of a cluster share a tile's K chunks.  The split that ends first, each
 // CTA costing its chunks and about four chunks' time for its start, its share
-// of the sum and its stores.
-int split_of(int tiles, int nk, const int (&slots)[9]) {
+// of the sum and its stores, and half as much again per chunk where CTAs have
+// to share SMs.  alone[s], shared[s]: clusters of s that run at once with one
+// and with two CTAs per SM.  (W [2048][5632], 16 tiles, 15 clusters of 8 and 23
+// of 6 alone: T = 32 from the L2 6.3 us split by 8, 5.4 by 6; from memory 8.3 and 8.7.)
+int split_of(int tiles, int nk, const int (&alone)[9], const int (&shared)[9]) {
   int best = 1;
   long long cost = -1;
   for (int s = 1; s <= 8 && s <= nk; ++s) {
-    const long long waves = (tiles + slots[s] - 1) / slots[s];   // slots[s] clusters of s at a time
-    const long long c = waves * ((nk + s - 1) / s + 4);
+    const long long rounds = (tiles + shared[s] - 1) / shared[s], chunks = (nk + s - 1) / s;
+    const long long c = rounds * (chunks * (tiles > alone[s] ? 3 : 2) + 8);
     if (cost < 0 || c < cost) {
       cost = c;
       best = s;
@@ -859,17 +870,20 @@ cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)((p.a.N + FT - 1) / FT) * ((p.a.T + NT - 1) / NT);
   const int nk = (p.a.K + kChunk / p.elem - 1) / (kChunk / p.elem);
-  static std::atomic<int> resident[kMaxDevices][9];   // clusters of s CTAs that run at once, asked once per device
-  int slots[9];
-  for (int s = 1; s <= 8; ++s) {
-    slots[s] = resident[p.dev][s].load(std::memory_order_relaxed);
-    if (!slots[s]) {
-      const cudaError_t q = active_clusters((const void*)kernel, C::kThreads, C::kSmem, s, &slots[s]);
-      if (q != cudaSuccess) return q;
-      resident[p.dev][s].store(slots[s], std::memory_order_relaxed);
+  // asked once per device; racing first calls ask twice and store the same
+  static std::atomic<int> known[kMaxDevices][2][9];
+  int fit[2][9];
+  for (int two = 0; two < 2; ++two)
+    for (int s = 1; s <= 8; ++s) {
+      int& n = fit[two][s];
+      n = known[p.dev][two][s].load(std::memory_order_relaxed);
+      if (!n) {
+        const cudaError_t q = active_clusters(C::kThreads, two ? C::kSmem : 200 * 1024, s, &n);
+        if (q != cudaSuccess) return q;
+        known[p.dev][two][s].store(n, std::memory_order_relaxed);
+      }
     }
-  }
-  const int S = tiles > (1 << 24) ? 1 : split_of((int)tiles, nk, slots);
+  const int S = tiles > (1 << 24) ? 1 : split_of((int)tiles, nk, fit[0], fit[1]);
   if (tiles * S > 0x7fffffff) return cudaErrorInvalidConfiguration;
   // Grids of more CTAs than SMs keep the memory busy to their end, and the next
   // grid's prefetch takes over there (W [11264][2048] FP16 9.8 -> 9.3 us);
@@ -892,7 +906,7 @@ cudaError_t launch_wide_o(const Problem& p, cudaStream_t st) {
   static std::atomic<int> resident[kMaxDevices];   // clusters that run at once, asked once per device
   int n = resident[p.dev].load(std::memory_order_relaxed);
   if (!n) {
-    e = active_clusters((const void*)kernel, C::kThreads, C::kSmem, 2 * PAIRS, &n);
+    e = active_clusters(C::kThreads, C::kSmem, 2 * PAIRS, &n);
     if (e != cudaSuccess) return e;
     resident[p.dev].store(n, std::memory_order_relaxed);
   }

@@ -17,7 +17,8 @@
 // tiles of a short problem): persistent CTA pairs (cta_group::2) over tiles
 // of 256 tokens x 256, 128 or 64 weight rows, two accumulators, so that one
 // tile's epilogue runs under the next tile's MMAs.
-// T = 2048, W [11264][2048]: E4M3 37 us (2,550 TFLOP/s), FP16 56 us (1,690).
+// T = 2048, W [11264][2048]: E4M3 33 us (2,840 TFLOP/s), FP16 55 us (1,710); T =
+// 4096, W [11264][5632] E4M3 140 us (3,700).
 #include <cuda.h>
 #include <atomic>
 
@@ -526,13 +527,17 @@ __global__ void __launch_bounds__(192, 2)
 // loads half of its 128 rows for itself and its counterpart (TMA multicast).
 // That saves a quarter of a 256-row tile's reads from the L2, a third of a
 // 128-row tile's.
-template <int BN>
+// WARPS epilogue warps: 16 for E4M3 SWIGLU with 256 rows, whose epilogue with 8
+// takes longer than a short K's MMAs (T = 2048, N = 5632: K = 2048 35.5 -> 33.3
+// us, with bias 40.6 -> 36.3; T = 4096, K = 5632 138 -> 140), else 8, whose
+// registers hold all of a chunk.
+template <int BN, int WARPS>
 struct WideCfg {
   static constexpr int kA = 128 * kChunk;   // the 128 token rows of this CTA
   static constexpr int kB = BN / 2 * kChunk;   // this CTA's half of the weight rows
   static constexpr int kStage = kA + kB;
-  static constexpr int kStages = 192 * 1024 / kStage;
-  static constexpr int kEpiWarps = 8;
+  static constexpr int kEpiWarps = WARPS, kParts = WARPS / 4;   // kParts warps per TMEM lane quarter
+  static constexpr int kStages = (224 - 4 * WARPS) * 1024 / kStage;
   static constexpr int kTurn = 32 * 32 * 4;   // per epilogue warp: 32 rows x 32 FP32 columns
   static constexpr int kBars = 2 * kStages + 4;
   static constexpr int kSmem = kStages * kStage + kEpiWarps * kTurn + kBars * 8 + 16 + 1024;
@@ -591,11 +596,14 @@ DEV_INLINE void finish_turned(const LinearArgs& a, const float* buf, int t0, int
   store_quads<O, kPass>(a, t, live, n0 + c, step, v);
 }
 
+template <bool F8, bool GATED, int BN>
+using WideFor = WideCfg<BN, F8 && GATED && BN == 256 ? 16 : 8>;
+
 template <bool F8, bool GATED, int BN, int PAIRS, typename O>
-__global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
+__global__ void __launch_bounds__(WideFor<F8, GATED, BN>::kThreads, 1)
     linear_wide_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmX) {
-  using C = WideCfg<BN>;
+  using C = WideFor<F8, GATED, BN>;
   constexpr int kElem = F8 ? 128 : 64;
   constexpr uint32_t kCols = 2 * BN;      // two accumulators
   constexpr int FT = GATED ? BN / 2 : BN;   // output features per tile
@@ -708,8 +716,8 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     }
     __syncwarp();
   } else {
-    // a TMEM lane (token) per thread; the two warps of a lane quarter take half
-    // of the tile's output features each
+    // a TMEM lane (token) per thread; the kParts warps of a lane quarter share
+    // the tile's output features
     const int q = warp & 3, h = (warp - 2) >> 2;
     float* buf = turn + (warp - 2) * (C::kTurn / 4);
     Pipe acc;
@@ -720,7 +728,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
       const uint32_t d = tmem + (uint32_t)(acc.i * BN) + ((uint32_t)(q * 32) << 16);
       const float xs = a.xs && t0 + lane < a.T ? a.xs[t0 + lane] : 1.f;
       constexpr int kStep = GATED ? 16 : 32;   // output features at a time
-      for (int c0 = h * (FT / 2); c0 < (h + 1) * (FT / 2); c0 += kStep) {
+      for (int c0 = h * (FT / C::kParts); c0 < (h + 1) * (FT / C::kParts); c0 += kStep) {
         if (t0 >= a.T || n0 + c0 >= a.N) break;   // the same for the whole warp
         uint32_t v[32];
         if constexpr (GATED) {
@@ -814,7 +822,7 @@ constexpr int kMaxDevices = 64;
 // Asked about below in the place of the kernels of its shape, never launched:
 // for a kernel that allocates tensor memory the occupancy query answers one
 // CTA per SM, whatever it allocates.
-__global__ void __launch_bounds__(320) shape_kernel() {}
+__global__ void __launch_bounds__(576) shape_kernel() {}
 
 // Clusters of CTAs of this shape that can be resident at once.  GPCs hold a
 // whole number of clusters: at one CTA per SM 76 of 2 but 36 of 4, at two 152 of
@@ -895,7 +903,7 @@ cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
 
 template <bool F8, bool GATED, int BN, int PAIRS, typename O>
 cudaError_t launch_wide_o(const Problem& p, cudaStream_t st) {
-  using C = WideCfg<BN>;
+  using C = WideFor<F8, GATED, BN>;
   CUtensorMap mw, mx;
   if (!encode_rows(&mw, p.w, GATED ? 2ll * p.a.N : p.a.N, p.a.K, p.elem, p.ld_w, BN / 2) ||
       !encode_rows(&mx, p.x, p.a.T, p.a.K, p.elem, p.ld_x, 128 / PAIRS))

@@ -166,7 +166,8 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_forward(moe_w4a16_handle* h, const void
  * or any other rule) instead of the handle's softmax router:
  *   out = (RESIDUAL ? x : 0) + sum_{j=0..k-1} topk_w[t][j] y(topk_ids[t][j])
  * with y as in moe_w4a16_forward and the ranks summed in j order in FP32.
- *   topk_ids [T][k] int32, topk_w [T][k] FP32: device, k = the handle's top_k.
+ *   topk_ids [T][k] int32, topk_w [T][k] FP32: device, k = the handle's top_k;
+ *   an id may occur more than once in a row.
  * Flags: RESIDUAL, FORCE_GEMV, FORCE_GEMM.  An absent expert contributes 0 and
  * counts as a miss; an id outside [0, E) counts as a miss too and is taken as
  * expert 0 with weight 0.  Runs as separate launches in every regime (1 or 3

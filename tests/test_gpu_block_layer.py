@@ -96,6 +96,26 @@ def test_routed_absent_experts_and_bad_ids(T, force):
         m.close()
 
 
+@pytest.mark.parametrize("T", [1, 2, 3, 7, 8, 9])
+@pytest.mark.parametrize("force", [F.FORCE_GEMV, F.FORCE_GEMM])
+def test_routed_one_expert_takes_every_pair(T, force):
+    """Up to k pairs of a token for one expert: repeated ids, and ids out of range (taken as expert 0)."""
+    layer = synth.make_layer(synth.LayerShape(hidden=2048, inter=256, num_experts=16, top_k=8), 78)
+    m = gp.make_handle(layer, 9)
+    try:
+        x = synth.draw_x(9, T, 2048)
+        w = np.full((T, 8), 0.125, np.float32)
+        for ids in (np.full((T, 8), 3), np.where(np.arange(8) < 5, 0, -1) + np.zeros((T, 1), int), np.full((T, 8), 16)):
+            ids = ids.astype(np.int32)
+            bad = int(((ids < 0) | (ids > 15)).sum())
+            out = m.forward_routed(gp.to_dev(x), gp.to_dev(ids), gp.to_dev(w), force)
+            assert m.get_status() == ((F.ERR_NOT_RESIDENT, bad) if bad else (F.OK, 0))
+            gp.assert_output(out.float().cpu().numpy().astype(np.float64), oracle_routed(layer, x, ids, w),
+                             np.ones(T, bool))
+    finally:
+        m.close()
+
+
 def test_routed_refusals(tiny):
     import torch
     _, m = tiny

@@ -49,8 +49,10 @@ __global__ void __launch_bounds__(256) gemv_gateup_kernel(FwdCtx c, int xrows) {
     bulk_g2s(smem, tile_ptr(base, LG, rt), TS, &bar);
     bulk_g2s(smem + TS, tile_ptr(base, c.lay.up, rt), TS, &bar);
   }
-  for (int p0 = 0; p0 < cnt; p0 += kTok) {
-    const int np = min(kTok, cnt - p0);
+  // xrows: as many rows as there is room for.  Usually an expert has at most one
+  // pair of each of T < kTok tokens; ids given by the caller may repeat.
+  for (int p0 = 0; p0 < cnt; p0 += xrows) {
+    const int np = min(xrows, cnt - p0);
     __syncthreads();   // previous pass done with xs / red / s_tok; barrier init visible
     if (tid < np) s_tok[tid] = c.sorted[start + p0 + tid] / c.k;
     __syncthreads();
@@ -132,8 +134,8 @@ __global__ void __launch_bounds__(256) gemv_down_kernel(FwdCtx c, int hrows) {
     const uint8_t* const tiles[2] = {smem + (size_t)half_sel * TS, nullptr};
     __half* hs = reinterpret_cast<__half*>(smem + 2 * (size_t)TS);
     float* red = reinterpret_cast<float*>(smem + 2 * (size_t)TS + (size_t)hrows * stride * sizeof(__half));
-    for (int p0 = 0; p0 < cnt; p0 += kTok) {
-      const int np = min(kTok, cnt - p0);
+    for (int p0 = 0; p0 < cnt; p0 += hrows) {   // as in the gate/up kernel
+      const int np = min(hrows, cnt - p0);
       __syncthreads();
       if (tid < np) s_rows[tid] = start + p0 + tid;
       __syncthreads();

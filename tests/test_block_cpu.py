@@ -101,6 +101,14 @@ def test_routed_forward_without_a_handle(lib):
     assert lib.moe_w4a16_forward_routed(None, P, 1, P, P, 0, P, None) == F.ERR_INVALID_ARG
 
 
+def test_routed_forward_refuses_host_tensors():
+    m = object.__new__(F.MoELayer)   # refused before the library is called
+    m.h, m.cfg = None, F.Config(hidden=64, inter=64, num_experts=4, top_k=2)
+    x, ids, w = torch.zeros(3, 64, dtype=torch.float16), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2)
+    with pytest.raises(ValueError, match="CUDA device"):
+        m.forward_routed(x, ids, w)
+
+
 def test_binding_refuses_wrong_tensors():
     x = torch.zeros(2, 64, dtype=torch.float16)
     for f in (lambda: B.add_rmsnorm(x), lambda: B.linear(x, x), lambda: B.route_scored(x, 2)):

@@ -222,7 +222,9 @@ class MoELayer:
         return (out, dbg) if debug else out
 
     def forward_routed(self, x, ids, weights, flags: int = 0, out=None, stream=None):
-        """The experts on given routing: x cuda fp16 [T, H], ids int32 and weights fp32 [T, top_k]."""
+        """The experts on given routing: x cuda fp16 [T, H], ids int32 and weights fp32 [T, top_k], on the layer's device.
+
+        An id may occur more than once in a row; one outside [0, E) contributes nothing and counts as a miss."""
         import torch
         T = int(x.shape[0])
         if ids.dtype != torch.int32 or weights.dtype != torch.float32 or ids.shape != (T, self.cfg.top_k) or \
@@ -230,8 +232,12 @@ class MoELayer:
             raise ValueError(f"ids (int32) and weights (float32) must have shape ({T}, {self.cfg.top_k})")
         if x.dtype != torch.float16 or x.dim() != 2 or x.shape[1] != self.cfg.hidden:
             raise ValueError(f"x must be float16 of shape (T, {self.cfg.hidden})")
+        if any(t.get_device() != self.cfg.device for t in (x, ids, weights)):
+            raise ValueError("x, ids and weights must be on the layer's CUDA device")
         if out is None:
             out = torch.empty_like(x)
+        elif out.dtype != x.dtype or out.shape != x.shape or out.device != x.device:
+            raise ValueError("out must have x's type, shape and device")
         self._check(self.lib.moe_w4a16_forward_routed(self.h, _ptr(x), T, _ptr(ids), _ptr(weights), flags, _ptr(out),
                                                       _stream(stream)))
         return out

@@ -557,7 +557,7 @@ typedef struct {
  * FP32, required for E4M3 and not allowed otherwise; bias FP32 or NULL;
  * residual [T][N] in out_dtype or NULL, may be out itself (same stride).
  * x and W must be 16-byte aligned with row strides of a multiple of 16 bytes
- * (N, K and T may be odd).  Products accumulate in FP32 on the tensor cores;
+ * (N, K and T may be odd; the stride of a single row is not used).  Products accumulate in FP32 on the tensor cores;
  * with few tokens K is split over the CTAs of a cluster and the parts are
  * added in a fixed order, so a call's result does not change from run to
  * run.  A bounded device wait that gave up is reported by

@@ -361,6 +361,24 @@ def test_linear_strides_guards_and_in_place_residual(T, off):
     check_linear(x, w, None, None, None, None, "gelu", got, r_in=keep)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16, E4], ids=["fp16", "bf16", "e4m3"])
+@pytest.mark.parametrize("T,N,K", [(1, 1, 1), (1, 1, 1001), (1, 130, 1001), (2, 1, 33), (17, 65, 77), (70, 129, 1001)])
+def test_linear_odd_k_and_single_rows(dtype, T, N, K):
+    """K off the 16-byte grid (rows padded to it), and single rows of x or W, whose stride counts for nothing."""
+    x, w, xs, ws, b, r = make_linear(T, N, K, dtype, "none", True, True, F32)
+    padded = []
+    for t in (x, w):
+        p = torch.full((t.shape[0], (K + 15) // 16 * 16), 7.0, device="cuda").to(dtype)   # never read as values
+        p[:, :K] = t
+        padded.append(p[:, :K] if t.shape[0] > 1 else p[0, :K].view(1, K))
+    x, w = padded
+    check_linear(x, w, xs, ws, b, r, "none",
+                 B.linear(x, w, x_scale=xs, w_scale=ws, bias=b, residual=r, out_dtype=F32))
+    if N > 1:   # no rows of x at all
+        none = B.linear(x[:0], w, x_scale=None if xs is None else xs[:0], w_scale=ws, out_dtype=F32)
+        assert none.shape == (0, N)
+
+
 def test_linear_same_result_every_run_and_nothing_left_over():
     """Runs twice over several splits; a large-valued call in between must leave no trace."""
     for T, N, K in ((1, 64, 4096), (16, 512, 2048), (100, 300, 1024), (400, 260, 512)):

@@ -1005,14 +1005,17 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linea
     return blk::reject(op, "out_dtype must be F16, BF16 or F32");
   if (c.act < MOE_W4A16_ACT_NONE || c.act > MOE_W4A16_ACT_SWIGLU) return blk::reject(op, "unknown activation");
   if (c.reserved) return blk::reject(op, "reserved must be 0");
-  if (c.n < 1 || c.n > (1 << 29) || c.k < 1 || c.k > (1 << 30))
-    return blk::reject(op, "n outside [1, 2^29] or k outside [1, 2^30]");
+  if (c.n < 1 || c.n > (1 << 29) || c.k < 1 || c.k > (1 << 24))   // at 2^24 a tile's chunks take
+    return blk::reject(op, "n outside [1, 2^29] or k outside [1, 2^24]");   // 0.1-0.2 s, a wait gives up after 1 s
   if (T < 0 || T > (1 << 30)) return blk::reject(op, "T outside [0, 2^30]");
   const int es = elem_size(c.in_dtype), os = elem_size(c.out_dtype);
-  const int64_t ld_x = c.ld_x ? c.ld_x : c.k, ld_w = c.ld_w ? c.ld_w : c.k;
+  int64_t ld_x = c.ld_x ? c.ld_x : c.k, ld_w = c.ld_w ? c.ld_w : c.k;
   const int64_t ld_out = c.ld_out ? c.ld_out : c.n, ld_res = c.ld_residual ? c.ld_residual : c.n;
   if (ld_x < c.k || ld_w < c.k || ld_out < c.n || ld_res < c.n)
     return blk::reject(op, "a row stride is below the row length");
+  // a single row has no stride to speak of: any that the tensor map takes
+  if (T < 2) ld_x = (c.k + 15ll) / 16 * 16;
+  if (c.n == 1 && c.act != MOE_W4A16_ACT_SWIGLU) ld_w = (c.k + 15ll) / 16 * 16;
   if (ld_x * es % 16 || ld_w * es % 16) return blk::reject(op, "the row strides of x and W must be multiples of 16 bytes");
   if (ld_x * es >= (1ll << 40) || ld_w * es >= (1ll << 40)) return blk::reject(op, "a row stride is too large");
   if (T == 0) return MOE_W4A16_OK;

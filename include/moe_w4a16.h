@@ -544,8 +544,8 @@ enum {
 typedef struct {
   int32_t in_dtype;     /* x and W: F16, BF16 or E4M3 */
   int32_t out_dtype;    /* out and residual: F16, BF16 or F32 */
-  int32_t n;            /* N: output features, >= 1 */
-  int32_t k;            /* K: input features, >= 1 */
+  int32_t n;            /* N: output features, 1..2^29 */
+  int32_t k;            /* K: input features, 1..2^24 */
   int32_t act;          /* MOE_W4A16_ACT_* */
   int32_t reserved;     /* 0 */
   int64_t ld_x, ld_w, ld_residual, ld_out;

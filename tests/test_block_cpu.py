@@ -78,6 +78,7 @@ def linear(lib, T=2, x=P, w=2 * P, xs=None, ws=None, bias=None, res=None, out=3 
 @pytest.mark.parametrize("kw,word", [
     (dict(in_dtype=2), "in_dtype"), (dict(out_dtype=3), "out_dtype"), (dict(act=6), "activation"),
     (dict(act=-1), "activation"), (dict(reserved=1), "reserved"), (dict(n=0), "n outside"), (dict(k=0), "n outside"),
+    (dict(n=(1 << 29) + 1), "n outside"), (dict(k=(1 << 24) + 8), "n outside"),
     (dict(T=-1), "T"), (dict(ld_x=63), "stride"), (dict(ld_out=63), "stride"), (dict(ld_residual=1), "stride"),
     (dict(k=60), "16 bytes"), (dict(ld_w=68), "16 bytes"), (dict(in_dtype=3, k=72, xs=P, ws=P), "16 bytes"),
     (dict(ld_x=1 << 40), "too large"), (dict(x=None), "NULL"), (dict(w=None), "NULL"), (dict(out=None), "NULL"),

@@ -8,7 +8,8 @@ The definitions, limits and masking rules are those of moe_w4a16_add_rmsnorm,
 moe_w4a16_linear and moe_w4a16_route_scored in include/moe_w4a16.h; this
 module and the compiled _block beside it check tensors and marshal pointers.
 Inputs are CUDA tensors of one device; a wrong shape, type or layout raises
-ValueError, an error of the library MoEError.  Rows may be strided (the last dimension contiguous).
+ValueError, an error of the library MoEError.  Rows may be strided (the last
+dimension contiguous).  There is no backward pass: outputs carry no gradient.
 Outputs are allocated unless given; with stream=None work goes to the
 current stream.
 """

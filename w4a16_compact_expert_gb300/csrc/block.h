@@ -5,6 +5,8 @@
 #include <cuda_fp8.h>
 #include <stdio.h>
 
+#include <atomic>
+
 #include "moe_w4a16.h"
 #include "internal.h"
 
@@ -45,19 +47,19 @@ inline moe_w4a16_status launch_failed(const char* op, cudaError_t e) {
 
 // SM count of the current device, asked once per device.
 inline int current_sms(int* device = nullptr) {
-  static int sms[64] = {};
+  static std::atomic<int> sms[64];   // racing first calls store the same
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();
     return 0;
   }
-  if (!sms[dev]) {
-    int n = 0;
+  int n = sms[dev].load(std::memory_order_relaxed);
+  if (!n) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) cudaGetLastError();
-    sms[dev] = n;
+    sms[dev].store(n, std::memory_order_relaxed);
   }
   if (device) *device = dev;
-  return sms[dev];
+  return n;
 }
 
 inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

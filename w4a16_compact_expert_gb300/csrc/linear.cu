@@ -20,7 +20,6 @@
 // T = 2048, W [11264][2048]: E4M3 33 us (2,840 TFLOP/s), FP16 55 us (1,710); T =
 // 4096, W [11264][5632] E4M3 140 us (3,700).
 #include <cuda.h>
-#include <atomic>
 
 #include "block.h"
 
@@ -994,7 +993,7 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linea
                                                            const void* x, const void* w, const float* x_scale,
                                                            const float* w_scale, const float* bias,
                                                            const void* residual, void* out,
-                                                           moe_w4a16_stream_t stream) {
+                                                           moe_w4a16_stream_t stream) try {
   const char* op = "linear";
   if (!cfg) return blk::reject(op, "cfg is NULL");
   const moe_w4a16_linear_config c = *cfg;
@@ -1055,6 +1054,8 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linea
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = f8 ? launch_linear<true>(p, st) : launch_linear<false>(p, st);
   return e == cudaSuccess ? MOE_W4A16_OK : blk::launch_failed(op, e);
+} catch (...) {   // the host's heap is full
+  return MOE_W4A16_ERR_OOM;
 }
 
 extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_block_status(void) {

@@ -418,7 +418,7 @@ Access access_of(const NormArgs& a) {
 
 extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_add_rmsnorm(
     const moe_w4a16_rmsnorm_config* cfg, int64_t T, const void* x, const void* residual, const void* weight,
-    void* residual_out, void* y, void* q, float* q_scale, moe_w4a16_stream_t stream) {
+    void* residual_out, void* y, void* q, float* q_scale, moe_w4a16_stream_t stream) try {
   const char* op = "add_rmsnorm";
   if (!cfg) return blk::reject(op, "cfg is NULL");
   const moe_w4a16_rmsnorm_config c = *cfg;
@@ -461,4 +461,6 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_add_rmsnorm(
   const cudaError_t e = c.dtype == MOE_W4A16_F16 ? launch_e<__half>(a, acc, num_sms, st)
                                                      : launch_e<__nv_bfloat16>(a, acc, num_sms, st);
   return e == cudaSuccess ? MOE_W4A16_OK : blk::launch_failed(op, e);
+} catch (...) {   // the host's heap is full
+  return MOE_W4A16_ERR_OOM;
 }

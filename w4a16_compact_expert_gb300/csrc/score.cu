@@ -15,11 +15,13 @@
 // could come out in the wrong order.  The FP32 pass therefore also checks
 // every border that decided something (between neighbours of the k chosen,
 // between the last chosen and all others, between kept and dropped groups)
-// against a bound of that error, and decides a closer one in FP64.  Usually only the experts at the border are taken up again in FP64,
-// one per lane: a whole token in FP64 takes a warp 16 us of dependent
-// operations, T = 2048, E = 256 with groups 13.5 us.  With no bias the experts are ordered by the logits themselves
-// (both scores are increasing in them), which is exact, so only group values
-// (sums of two scores) need the check.
+// against a bound of that error, and decides a closer one in FP64.  Usually
+// only the experts at the border are taken up again in FP64, one per lane: a
+// whole token in FP64 takes a warp 16 us of dependent operations (when every
+// close token went that way, T = 2048, E = 256 with groups took 13.5 us).
+// With no bias the experts are ordered by the logits themselves (both scores
+// are increasing in them), which is exact, so only group values (sums of two
+// scores) need the check.
 #include "block.h"
 
 namespace {
@@ -550,7 +552,7 @@ cudaError_t launch_e(const ScoreArgs& a, cudaStream_t st) {
 extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_route_scored(const moe_w4a16_route_config* cfg, int64_t T,
                                                                  const void* logits, const float* bias,
                                                                  int32_t* topk_ids, float* topk_w,
-                                                                 moe_w4a16_stream_t stream) {
+                                                                 moe_w4a16_stream_t stream) try {
   const char* op = "route_scored";
   if (!cfg) return blk::reject(op, "cfg is NULL");
   const moe_w4a16_route_config c = *cfg;
@@ -598,4 +600,6 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_route_scored(const moe_w4a16
                         : c.dtype == MOE_W4A16_F16 ? launch_e<__half>(a, st)
                                                    : launch_e<__nv_bfloat16>(a, st);
   return e == cudaSuccess ? MOE_W4A16_OK : blk::launch_failed(op, e);
+} catch (...) {   // the host's heap is full
+  return MOE_W4A16_ERR_OOM;
 }

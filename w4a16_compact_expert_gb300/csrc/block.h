@@ -24,6 +24,19 @@ DEV_INLINE __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfl
 template <>
 DEV_INLINE float from_float<float>(float v) { return v; }
 
+// One instruction each beside the multiplication; results below 2^-126 are 0.
+// e^x as 2^(x log2 e): relative error |x| 2^-24 + 2 ulp; 1 / x: 1 ulp, 0 where |x| passes 2^126.
+DEV_INLINE float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+DEV_INLINE float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // W neighbouring elements, loaded and stored at once.
 template <typename E, int W>
 struct alignas(sizeof(E) * W) Pack {

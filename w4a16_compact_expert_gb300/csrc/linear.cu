@@ -41,7 +41,7 @@ struct LinearArgs {
 };
 
 // a / (1 + e^-a); the quotient is 0 where e^-a passes 2^126, as it should be.
-DEV_INLINE float silu(float a) { return __fdividef(a, 1.f + __expf(-a)); }
+DEV_INLINE float silu(float a) { return a * blk::fast_rcp(1.f + blk::fast_exp(-a)); }
 
 // a Phi(a) with the normal distribution's Phi(-|a|) = erfc(|a| / sqrt 2) / 2 by
 // formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions
@@ -49,17 +49,17 @@ DEV_INLINE float silu(float a) { return __fdividef(a, 1.f + __expf(-a)); }
 // a keep their relative accuracy.
 DEV_INLINE float gelu(float a) {
   const float z = fabsf(a) * 0.70710678f;
-  const float t = __fdividef(1.f, fmaf(0.3275911f, z, 1.f));
+  const float t = blk::fast_rcp(fmaf(0.3275911f, z, 1.f));
   const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
                            0.254829592f);
-  const float tail = 0.5f * p * __expf(-z * z);   // Phi(-|a|)
+  const float tail = 0.5f * p * blk::fast_exp(-z * z);   // Phi(-|a|)
   return a * (a > 0.f ? 1.f - tail : tail);
 }
 
 // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
 DEV_INLINE float gelu_tanh(float a) {
   const float u = 0.7978845608f * fmaf(0.044715f * a, a * a, a);
-  return __fdividef(a, 1.f + __expf(-2.f * u));
+  return a * blk::fast_rcp(1.f + blk::fast_exp(-2.f * u));
 }
 
 // The switch stands outside the values' loop: one branch per value kept a

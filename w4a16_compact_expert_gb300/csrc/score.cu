@@ -67,12 +67,6 @@ DEV_INLINE float warp_max_f(float v) {
   return v;
 }
 
-DEV_INLINE float fast_exp(float x) {   // 2^(x log2 e): relative error |x| 2^-24 + 2 ulp
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
-  return r;
-}
-
 template <typename E>
 DEV_INLINE float logit_at(const ScoreArgs& a, long long t, int e) {
   const float v = blk::to_float(static_cast<const E*>(a.logits)[t * a.ld + e]);
@@ -278,7 +272,7 @@ DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
     if (scored || !a.renorm) {
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) s += l[i] == -INFINITY ? 0.f : l[i] == m ? 1.f : fast_exp(l[i] - m);
+      for (int i = 0; i < EPL; ++i) s += l[i] == -INFINITY ? 0.f : l[i] == m ? 1.f : blk::fast_exp(l[i] - m);
       den = warp_sum(s);
     }
   }
@@ -298,8 +292,8 @@ DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
     float c = l[i];
     if (a.bias) {
       const float b = e0 + i < a.E ? a.bias[e0 + i] : 0.f;
-      const float s = a.sigmoid ? __fdividef(1.f, 1.f + fast_exp(fminf(-l[i], 80.f)))
-                                : (l[i] == m ? 1.f : fast_exp(l[i] - m)) * inv_den;
+      const float s = a.sigmoid ? blk::fast_rcp(1.f + blk::fast_exp(fminf(-l[i], 80.f)))
+                                : (l[i] == m ? 1.f : blk::fast_exp(l[i] - m)) * inv_den;
       c = l[i] == -INFINITY || !(b > -INFINITY) ? -INFINITY : s + b;
     }
     key[i] = e0 + i < a.E ? key_of(c) : 0u;

@@ -24,17 +24,43 @@ DEV_INLINE __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfl
 template <>
 DEV_INLINE float from_float<float>(float v) { return v; }
 
-// One instruction each beside the multiplication; results below 2^-126 are 0.
-// e^x as 2^(x log2 e): relative error |x| 2^-24 + 2 ulp; 1 / x: 1 ulp, 0 where |x| passes 2^126.
-DEV_INLINE float fast_exp(float x) {
+// One instruction each (e^x: beside the multiplication); results below 2^-126
+// are 0.  2^x: 2 ulp; e^x as 2^(x log2 e): |x| 2^-24 more, relative; 1 / x: 1
+// ulp, 0 where |x| passes 2^126.
+DEV_INLINE float fast_exp2(float x) {
   float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+DEV_INLINE float fast_exp(float x) { return fast_exp2(x * 1.4426950408889634f); }
 DEV_INLINE float fast_rcp(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// Packed FP32 pairs.
+DEV_INLINE float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+DEV_INLINE float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+DEV_INLINE float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<unsigned long long*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
 }
 
 // W neighbouring elements, loaded and stored at once.

@@ -14,6 +14,9 @@
 namespace {
 
 using blk::Pack;
+using blk::add2;
+using blk::fma2;
+using blk::mul2;
 
 struct NormArgs {
   const void *x, *res, *w;
@@ -37,30 +40,6 @@ enum Access {
 
 template <typename E>
 using Win = Pack<E, 8>;
-
-// Packed FP32 pairs.
-DEV_INLINE float2 mul2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-  return *reinterpret_cast<float2*>(&r);
-}
-DEV_INLINE float2 add2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-  return *reinterpret_cast<float2*>(&r);
-}
-DEV_INLINE float2 fma2(float2 a, float2 b, float2 c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
-        "l"(*reinterpret_cast<unsigned long long*>(&c)));
-  return *reinterpret_cast<float2*>(&r);
-}
 
 DEV_INLINE float2 pair_of(const Win<__half>& w, int j) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w.v[2 * j]));

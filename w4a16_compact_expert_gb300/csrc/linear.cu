@@ -20,6 +20,7 @@
 // T = 2048, W [11264][2048]: E4M3 33 us (2,840 TFLOP/s), FP16 55 us (1,710); T =
 // 4096, W [11264][5632] E4M3 140 us (3,700).
 #include <cuda.h>
+#include <type_traits>
 
 #include "block.h"
 
@@ -214,7 +215,10 @@ DEV_INLINE void store_quads(const LinearArgs& a, const int (&t)[Q], const bool (
     if (res) {
 #pragma unroll
       for (int q = 0; q < Q; ++q)
-        if (live[q]) o[q] = *reinterpret_cast<const blk::Pack<O, 4>*>(res + (size_t)t[q] * a.ld_res + n);
+        if (live[q]) {   // past the L1, which the shared memory leaves almost nothing
+          using V = typename std::conditional<sizeof(O) == 4, uint4, uint2>::type;
+          *reinterpret_cast<V*>(&o[q]) = __ldcg(reinterpret_cast<const V*>(res + (size_t)t[q] * a.ld_res + n));
+        }
 #pragma unroll
       for (int q = 0; q < Q; ++q)
 #pragma unroll
@@ -253,37 +257,48 @@ DEV_INLINE void store_quads(const LinearArgs& a, const int (&t)[Q], const bool (
   }
 }
 
-// Scales, bias and activation of quads whose columns are n + j step; g holds
-// the (gate) sums, u the up sums, already times the token's x_scale.
-template <bool GATED, int Q>
-DEV_INLINE void activate_quads(const LinearArgs& a, int n, int step, float (&g)[Q * 4], float (&u)[GATED ? Q * 4 : 1]) {
-  int nn[4];
+// Four columns n + j step; those past N repeat the last.
+struct Columns {
+  int n[4];
+  DEV_INLINE Columns(const LinearArgs& a, int first, int step) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) nn[j] = min(n + j * step, a.N - 1);
+    for (int j = 0; j < 4; ++j) n[j] = min(first + j * step, a.N - 1);
+  }
+};
+struct Four {   // their scales or biases
+  float v[4];
+};
+DEV_INLINE Four load_columns(const float* p, const Columns& c) {
+  Four f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f.v[j] = p[c.n[j]];
+  return f;
+}
+
+// Scales, bias and activation of Q quads; g holds the (gate) sums, u the up
+// sums, already times the token's x_scale.  w(up), b(up): the scales and biases
+// of the quads' columns (up: of the up rows), asked for one after the other as
+// they are needed.
+template <bool GATED, int Q, typename W, typename Bi>
+DEV_INLINE void activate_quads(const LinearArgs& a, W w, Bi b, float (&g)[Q * 4], float (&u)[GATED ? Q * 4 : 1]) {
   if (a.ws) {
-    float w[4];
+    const Four f = w(false);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = a.ws[nn[j]];
-#pragma unroll
-    for (int i = 0; i < Q * 4; ++i) g[i] *= w[i % 4];
+    for (int i = 0; i < Q * 4; ++i) g[i] *= f.v[i % 4];
     if constexpr (GATED) {
+      const Four h = w(true);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = a.ws[a.N + nn[j]];
-#pragma unroll
-      for (int i = 0; i < Q * 4; ++i) u[i] *= w[i % 4];
+      for (int i = 0; i < Q * 4; ++i) u[i] *= h.v[i % 4];
     }
   }
   if (a.bias) {
-    float b[4];
+    const Four f = b(false);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = a.bias[nn[j]];
-#pragma unroll
-    for (int i = 0; i < Q * 4; ++i) g[i] += b[i % 4];
+    for (int i = 0; i < Q * 4; ++i) g[i] += f.v[i % 4];
     if constexpr (GATED) {
+      const Four h = b(true);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = a.bias[a.N + nn[j]];
-#pragma unroll
-      for (int i = 0; i < Q * 4; ++i) u[i] += b[i % 4];
+      for (int i = 0; i < Q * 4; ++i) u[i] += h.v[i % 4];
     }
   }
   if constexpr (GATED) {
@@ -486,7 +501,14 @@ __global__ void __launch_bounds__(192, 2)
   const int step = wide ? 1 : kQ, f = (int)(threadIdx.x % kQ) * (wide ? 4 : 1), n = n0 + f;
   const int own = (nt - rank + S - 1) / S;   // tokens of this CTA
   const float* parts = reinterpret_cast<const float*>(smem + C::kRecvAt) + f;
-  if (n < a.N)
+  if (n < a.N) {
+    Four cw[GATED ? 2 : 1], cb[GATED ? 2 : 1];   // of the gate rows, of the up rows
+    const Columns at(a, n, step);
+#pragma unroll
+    for (int up = 0; up <= GATED; ++up) {
+      if (a.ws) cw[up] = load_columns(a.ws + up * a.N, at);
+      if (a.bias) cb[up] = load_columns(a.bias + up * a.N, at);
+    }
     for (int s = (int)threadIdx.x / kQ; s < own; s += kSweep * kBatch) {
       int t[kBatch];
       bool live[kBatch];
@@ -525,11 +547,13 @@ __global__ void __launch_bounds__(192, 2)
           }
         }
       }
-      activate_quads<GATED, kBatch>(a, n, step, v, up);
+      activate_quads<GATED, kBatch>(
+          a, [&](bool of_up) { return cw[GATED && of_up]; }, [&](bool of_up) { return cb[GATED && of_up]; }, v, up);
       if (out_dtype == MOE_W4A16_F16) store_quads<__half, kBatch>(a, t, live, n, step, v);
       else if (out_dtype == MOE_W4A16_BF16) store_quads<__nv_bfloat16, kBatch>(a, t, live, n, step, v);
       else store_quads<float, kBatch>(a, t, live, n, step, v);
     }
+  }
 }
 
 // -------------------------------------------------------------------- wide
@@ -565,8 +589,11 @@ struct WideCfg {
 // columns of 8 (GATED: 4) rows, 64- or 128-byte pieces of a row per store;
 // outputs that cannot be stored four at a time have a lane's columns
 // kLanes apart, so that the lanes' single stores still lie side by side.
+// cw, cb (not with GATED): the scales and biases of this warp's columns of the
+// tile, fetched ahead; chunk: which 32 of them.
 template <bool GATED, typename O>
-DEV_INLINE void finish_turned(const LinearArgs& a, const float* buf, int t0, int n0, int lane) {
+DEV_INLINE void finish_turned(const LinearArgs& a, const float* buf, int t0, int n0, int lane, const Four& cw,
+                              const Four& cb, int chunk) {
   constexpr int kLanes = GATED ? 4 : 8;    // lanes along a row
   constexpr int kPass = GATED ? 4 : 8, kRows = 32 / kPass;
   const bool wide = a.vec == 4 && n0 + 4 * kLanes <= a.N;
@@ -598,7 +625,16 @@ DEV_INLINE void finish_turned(const LinearArgs& a, const float* buf, int t0, int
       }
     }
   }
-  activate_quads<GATED, kPass>(a, n0 + c, step, v, w);
+  const Columns at(a, n0 + c, step);
+  auto columns = [&](const float* p, const Four& ahead, bool up) {
+    if (GATED) return load_columns(p + (up ? a.N : 0), at);
+    Four f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f.v[j] = __shfl_sync(0xffffffffu, ahead.v[j], chunk * kLanes + u);
+    return f;
+  };
+  activate_quads<GATED, kPass>(
+      a, [&](bool up) { return columns(a.ws, cw, up); }, [&](bool up) { return columns(a.bias, cb, up); }, v, w);
   int t[kPass];
   bool live[kPass];
 #pragma unroll
@@ -735,13 +771,34 @@ __global__ void __launch_bounds__(WideFor<F8, GATED, BN>::kThreads, 1)
     float* buf = turn + (warp - 2) * (C::kTurn / 4);
     Pipe acc;
     for (int tile = first; tile < tiles; tile += step) {
+      const int t0 = (tile % mtiles) * 256 + rank * 128 + q * 32, n0 = (tile / mtiles * PAIRS + pair) * FT;
+      constexpr int kStep = GATED ? 16 : 32, kLanes = kStep / 4, kPart = FT / C::kParts;
+      // Under the tile's MMAs: this warp's part of the residual starts towards
+      // the L2 (a lane takes a row), and its rows' scales (one to a lane) and its
+      // columns' scales and biases (four to a lane: lane chunk kLanes + u holds
+      // those of lane u of the chunk's rows) are fetched.  T = 2048, N = 2048, K =
+      // 1024 FP16 with residual 14.4 -> 13.1 us, with bias 11.8 -> 11.5; T = 2048,
+      // N = 4096, K = 2048 E4M3 18.8 -> 17.0.  SWIGLU has no registers to spare
+      // (E4M3, N = 5632, K = 2048 34.2 -> 37.9 us): its columns' as they are needed.
+      if (a.res && t0 + lane < a.T) {
+        const int n = n0 + h * kPart, left = min(kPart, a.N - n);
+        const O* p = static_cast<const O*>(a.res) + (size_t)(t0 + lane) * a.ld_res + n;
+        for (int c = 0; c < left; c += 128 / (int)sizeof(O)) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c) : "memory");
+      }
+      const float xs = a.xs && t0 + lane < a.T ? a.xs[t0 + lane] : 1.f;
+      Four cw = {}, cb = {};
+      if (!GATED && lane < kPart / 4) {
+        const int cn = n0 + h * kPart + lane / kLanes * kStep;
+        const bool wide = a.vec == 4 && cn + kStep <= a.N;
+        const Columns at(a, cn + (wide ? 4 * (lane % kLanes) : lane % kLanes), wide ? 1 : kLanes);
+        if (a.ws) cw = load_columns(a.ws, at);
+        if (a.bias) cb = load_columns(a.bias, at);
+      }
+      __syncwarp();
       if (!mbar_wait_bounded(&acc_full[acc.i], acc.ph, &g_block_status)) break;
       tc_fence_after();
-      const int t0 = (tile % mtiles) * 256 + rank * 128 + q * 32, n0 = (tile / mtiles * PAIRS + pair) * FT;
       const uint32_t d = tmem + (uint32_t)(acc.i * BN) + ((uint32_t)(q * 32) << 16);
-      const float xs = a.xs && t0 + lane < a.T ? a.xs[t0 + lane] : 1.f;
-      constexpr int kStep = GATED ? 16 : 32;   // output features at a time
-      for (int c0 = h * (FT / C::kParts); c0 < (h + 1) * (FT / C::kParts); c0 += kStep) {
+      for (int c0 = h * kPart; c0 < (h + 1) * kPart; c0 += kStep) {   // kStep output features at a time
         if (t0 >= a.T || n0 + c0 >= a.N) break;   // the same for the whole warp
         uint32_t v[32];
         if constexpr (GATED) {
@@ -767,7 +824,7 @@ __global__ void __launch_bounds__(WideFor<F8, GATED, BN>::kThreads, 1)
           *reinterpret_cast<uint4*>(buf + lane * 32 + ((j ^ (lane & 7)) * 4)) =
               make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         __syncwarp();
-        finish_turned<GATED, O>(a, buf, t0, n0 + c0, lane);
+        finish_turned<GATED, O>(a, buf, t0, n0 + c0, lane, cw, cb, (c0 - h * kPart) / kStep);
         __syncwarp();
       }
       tc_fence_before();

@@ -257,21 +257,14 @@ DEV_INLINE void store_quads(const LinearArgs& a, const int (&t)[Q], const bool (
   }
 }
 
-// Four columns n + j step; those past N repeat the last.
-struct Columns {
-  int n[4];
-  DEV_INLINE Columns(const LinearArgs& a, int first, int step) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) n[j] = min(first + j * step, a.N - 1);
-  }
-};
-struct Four {   // their scales or biases
+// Scales or biases of the columns n + j step; those past N repeat the last.
+struct Four {
   float v[4];
 };
-DEV_INLINE Four load_columns(const float* p, const Columns& c) {
+DEV_INLINE Four load_columns(const LinearArgs& a, const float* p, int n, int step) {
   Four f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) f.v[j] = p[c.n[j]];
+  for (int j = 0; j < 4; ++j) f.v[j] = p[min(n + j * step, a.N - 1)];
   return f;
 }
 
@@ -503,11 +496,10 @@ __global__ void __launch_bounds__(192, 2)
   const float* parts = reinterpret_cast<const float*>(smem + C::kRecvAt) + f;
   if (n < a.N) {
     Four cw[GATED ? 2 : 1], cb[GATED ? 2 : 1];   // of the gate rows, of the up rows
-    const Columns at(a, n, step);
 #pragma unroll
     for (int up = 0; up <= GATED; ++up) {
-      if (a.ws) cw[up] = load_columns(a.ws + up * a.N, at);
-      if (a.bias) cb[up] = load_columns(a.bias + up * a.N, at);
+      if (a.ws) cw[up] = load_columns(a, a.ws + up * a.N, n, step);
+      if (a.bias) cb[up] = load_columns(a, a.bias + up * a.N, n, step);
     }
     for (int s = (int)threadIdx.x / kQ; s < own; s += kSweep * kBatch) {
       int t[kBatch];
@@ -564,17 +556,13 @@ __global__ void __launch_bounds__(192, 2)
 // loads half of its 128 rows for itself and its counterpart (TMA multicast).
 // That saves a quarter of a 256-row tile's reads from the L2, a third of a
 // 128-row tile's.
-// WARPS epilogue warps: 16 for E4M3 SWIGLU with 256 rows, whose epilogue with 8
-// takes longer than a short K's MMAs (T = 2048, N = 5632: K = 2048 35.5 -> 33.3
-// us, with bias 40.6 -> 36.3; T = 4096, K = 5632 138 -> 140), else 8, whose
-// registers hold all of a chunk.
-template <int BN, int WARPS>
+template <int BN>
 struct WideCfg {
   static constexpr int kA = 128 * kChunk;   // the 128 token rows of this CTA
   static constexpr int kB = BN / 2 * kChunk;   // this CTA's half of the weight rows
   static constexpr int kStage = kA + kB;
-  static constexpr int kEpiWarps = WARPS, kParts = WARPS / 4;   // kParts warps per TMEM lane quarter
-  static constexpr int kStages = (224 - 4 * WARPS) * 1024 / kStage;
+  static constexpr int kStages = 192 * 1024 / kStage;
+  static constexpr int kEpiWarps = 8, kParts = kEpiWarps / 4;   // kParts warps per TMEM lane quarter
   static constexpr int kTurn = 32 * 32 * 4;   // per epilogue warp: 32 rows x 32 FP32 columns
   static constexpr int kBars = 2 * kStages + 4;
   static constexpr int kSmem = kStages * kStage + kEpiWarps * kTurn + kBars * 8 + 16 + 1024;
@@ -589,8 +577,8 @@ struct WideCfg {
 // columns of 8 (GATED: 4) rows, 64- or 128-byte pieces of a row per store;
 // outputs that cannot be stored four at a time have a lane's columns
 // kLanes apart, so that the lanes' single stores still lie side by side.
-// cw, cb (not with GATED): the scales and biases of this warp's columns of the
-// tile, fetched ahead; chunk: which 32 of them.
+// cw, cb: the scales and biases of this warp's columns of the tile, fetched
+// ahead; chunk: which 32 (GATED: 16) of them.
 template <bool GATED, typename O>
 DEV_INLINE void finish_turned(const LinearArgs& a, const float* buf, int t0, int n0, int lane, const Four& cw,
                               const Four& cb, int chunk) {
@@ -625,16 +613,14 @@ DEV_INLINE void finish_turned(const LinearArgs& a, const float* buf, int t0, int
       }
     }
   }
-  const Columns at(a, n0 + c, step);
-  auto columns = [&](const float* p, const Four& ahead, bool up) {
-    if (GATED) return load_columns(p + (up ? a.N : 0), at);
+  auto columns = [&](const Four& of, bool up) {
     Four f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f.v[j] = __shfl_sync(0xffffffffu, ahead.v[j], chunk * kLanes + u);
+    for (int j = 0; j < 4; ++j) f.v[j] = __shfl_sync(0xffffffffu, of.v[j], (up ? 16 : 0) + chunk * kLanes + u);
     return f;
   };
   activate_quads<GATED, kPass>(
-      a, [&](bool up) { return columns(a.ws, cw, up); }, [&](bool up) { return columns(a.bias, cb, up); }, v, w);
+      a, [&](bool up) { return columns(cw, up); }, [&](bool up) { return columns(cb, up); }, v, w);
   int t[kPass];
   bool live[kPass];
 #pragma unroll
@@ -645,14 +631,11 @@ DEV_INLINE void finish_turned(const LinearArgs& a, const float* buf, int t0, int
   store_quads<O, kPass>(a, t, live, n0 + c, step, v);
 }
 
-template <bool F8, bool GATED, int BN>
-using WideFor = WideCfg<BN, F8 && GATED && BN == 256 ? 16 : 8>;
-
 template <bool F8, bool GATED, int BN, int PAIRS, typename O>
-__global__ void __launch_bounds__(WideFor<F8, GATED, BN>::kThreads, 1)
+__global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     linear_wide_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmX) {
-  using C = WideFor<F8, GATED, BN>;
+  using C = WideCfg<BN>;
   constexpr int kElem = F8 ? 128 : 64;
   constexpr uint32_t kCols = 2 * BN;      // two accumulators
   constexpr int FT = GATED ? BN / 2 : BN;   // output features per tile
@@ -775,11 +758,12 @@ __global__ void __launch_bounds__(WideFor<F8, GATED, BN>::kThreads, 1)
       constexpr int kStep = GATED ? 16 : 32, kLanes = kStep / 4, kPart = FT / C::kParts;
       // Under the tile's MMAs: this warp's part of the residual starts towards
       // the L2 (a lane takes a row), and its rows' scales (one to a lane) and its
-      // columns' scales and biases (four to a lane: lane chunk kLanes + u holds
-      // those of lane u of the chunk's rows) are fetched.  T = 2048, N = 2048, K =
-      // 1024 FP16 with residual 14.4 -> 13.1 us, with bias 11.8 -> 11.5; T = 2048,
-      // N = 4096, K = 2048 E4M3 18.8 -> 17.0.  SWIGLU has no registers to spare
-      // (E4M3, N = 5632, K = 2048 34.2 -> 37.9 us): its columns' as they are needed.
+      // columns' scales and biases are fetched, four to a lane: lane chunk kLanes
+      // + u holds those of lane u of the chunk's rows (GATED: of the gate rows in
+      // the lanes below 16, of the up rows above).  T = 2048, N = 2048, K = 1024
+      // FP16 with residual 14.4 -> 13.1 us, with bias 11.8 -> 11.5; T = 2048, N =
+      // 4096, K = 2048 E4M3 18.8 -> 17.0; SWIGLU N = 5632 E4M3 35.5 -> 33.1, with
+      // bias 40.6 -> 35.0.
       if (a.res && t0 + lane < a.T) {
         const int n = n0 + h * kPart, left = min(kPart, a.N - n);
         const O* p = static_cast<const O*>(a.res) + (size_t)(t0 + lane) * a.ld_res + n;
@@ -787,12 +771,14 @@ __global__ void __launch_bounds__(WideFor<F8, GATED, BN>::kThreads, 1)
       }
       const float xs = a.xs && t0 + lane < a.T ? a.xs[t0 + lane] : 1.f;
       Four cw = {}, cb = {};
-      if (!GATED && lane < kPart / 4) {
-        const int cn = n0 + h * kPart + lane / kLanes * kStep;
+      static_assert(kPart / 4 <= (GATED ? 16 : 32), "a lane for every four columns");
+      const int cl = GATED ? lane & 15 : lane, up = GATED && lane >= 16 ? a.N : 0;
+      if (cl < kPart / 4) {
+        const int cn = n0 + h * kPart + cl / kLanes * kStep;
         const bool wide = a.vec == 4 && cn + kStep <= a.N;
-        const Columns at(a, cn + (wide ? 4 * (lane % kLanes) : lane % kLanes), wide ? 1 : kLanes);
-        if (a.ws) cw = load_columns(a.ws, at);
-        if (a.bias) cb = load_columns(a.bias, at);
+        const int n = cn + cl % kLanes * (wide ? 4 : 1), apart = wide ? 1 : kLanes;
+        if (a.ws) cw = load_columns(a, a.ws + up, n, apart);
+        if (a.bias) cb = load_columns(a, a.bias + up, n, apart);
       }
       __syncwarp();
       if (!mbar_wait_bounded(&acc_full[acc.i], acc.ph, &g_block_status)) break;
@@ -892,7 +878,7 @@ constexpr int kMaxDevices = 64;
 // Asked about below in the place of the kernels of its shape, never launched:
 // for a kernel that allocates tensor memory the occupancy query answers one
 // CTA per SM, whatever it allocates.
-__global__ void __launch_bounds__(576) shape_kernel() {}
+__global__ void __launch_bounds__(320) shape_kernel() {}
 
 // Clusters of CTAs of this shape that can be resident at once.  GPCs hold a
 // whole number of clusters: at one CTA per SM 76 of 2 but 36 of 4, at two 152 of
@@ -973,7 +959,7 @@ cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
 
 template <bool F8, bool GATED, int BN, int PAIRS, typename O>
 cudaError_t launch_wide_o(const Problem& p, cudaStream_t st) {
-  using C = WideFor<F8, GATED, BN>;
+  using C = WideCfg<BN>;
   CUtensorMap mw, mx;
   if (!encode_rows(&mw, p.w, GATED ? 2ll * p.a.N : p.a.N, p.a.K, p.elem, p.ld_w, BN / 2) ||
       !encode_rows(&mx, p.x, p.a.T, p.a.K, p.elem, p.ld_x, 128 / PAIRS))

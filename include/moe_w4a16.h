@@ -84,7 +84,7 @@ typedef enum {
   MOE_W4A16_OK = 0,
   MOE_W4A16_ERR_INVALID_ARG = 1,   /* bad pointer, shape, index or flag */
   MOE_W4A16_ERR_CUDA = 2,          /* a CUDA runtime call failed (message in last_error) */
-  MOE_W4A16_ERR_OOM = 3,           /* device allocation failed at create */
+  MOE_W4A16_ERR_OOM = 3,           /* device allocation failed at create, or no host memory */
   MOE_W4A16_ERR_NOT_PACKED = 4,    /* the slot table names a slot never packed */
   MOE_W4A16_ERR_NOT_RESIDENT = 5,  /* get_status: a routed expert had no slot */
   MOE_W4A16_ERR_TIMEOUT = 6,       /* get_status: a bounded device wait gave up */

@@ -336,14 +336,23 @@ DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
       b2 = max(min(b1, o1), max(b2, o2));
       b1 = max(b1, o1);
     }
-    float gv = of_key(max(b1, kNone));
+    // The group's value and a bound of its FP32 error: half of `slack` for each
+    // choice's score, and the roundings of the choices and of their sum, a unit
+    // each and taken twice, which count by the choices' own size: of opposite
+    // sign they may cancel.  With an eligible expert the value is never -inf,
+    // also where the sum overflows.
+    float gv = of_key(max(b1, kNone)), err = 0.5f * slack + 4.f * unit * fabsf(gv);
     if (a.two) {
       float v2 = of_key(max(b2, kNone));
       if (!a.bias && gv != -INFINITY) {   // keys of logits: their scores
         gv = score_of(a, gv, m, den);
         if (v2 != -INFINITY) v2 = score_of(a, v2, m, den);
       }
-      if (v2 != -INFINITY) gv += v2;
+      err = 0.5f * slack + 4.f * unit * fabsf(gv);
+      if (v2 != -INFINITY) {
+        err += 0.5f * slack + 4.f * unit * fabsf(v2);
+        gv = fmaxf(gv + v2, -3.402823466e38f);
+      }
     }
     int rank = 0;   // how many groups come before
     for (int o = 0; o < a.G; ++o) {
@@ -352,19 +361,22 @@ DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
     }
     bool kept = g < a.G && rank < a.top_groups;
     if (scored) {
-      const float least = -warp_max_f(kept ? -gv : -INFINITY), most = warp_max_f(g < a.G && !kept ? gv : -INFINITY);
-      const float far = (a.two ? 2.f : 1.f) * slack + 4.f * unit * fabsf(least);
-      if (most != -INFINITY && least - most <= far) {   // the same in every lane
+      // the 64-bit value lies between lo and hi; a kept group that may lie below
+      // a dropped one makes the border a close one
+      const bool none = gv == -INFINITY, sure = fabsf(gv) < 3.402823466e38f && err < INFINITY;
+      const float lo = sure ? gv - err : none ? gv : -3.402823466e38f, hi = sure ? gv + err : none ? gv : INFINITY;
+      const float least = -warp_max_f(kept ? -lo : -INFINITY), most = warp_max_f(g < a.G && !kept ? hi : -INFINITY);
+      if (most != -INFINITY && least <= most) {   // the same in every lane
         if (!whole) return true;
         // the groups on either side of the border in FP64, from their experts
         // that may be among the largest
         if (!a.sigmoid && den64 < 0.0) den64 = exact_den<E>(a, t, (double)m);
-        const bool border = g < a.G && gv != -INFINITY && (kept ? gv - most <= far : least - gv <= far);
+        const bool border = g < a.G && gv != -INFINITY && (kept ? lo <= most : hi >= least);
         const float low = of_key(max(a.two ? b2 : b1, kNone));
         unsigned long long x1 = 0ull, x2 = 0ull;
         for (int i = 0; i < EPL; ++i) {
           const uint32_t ki = border && e0 + i < a.E ? key_at(key, i) : 0u;
-          const bool may = ki > kNone && of_key(ki) >= low - (a.bias ? slack + 4.f * unit * fabsf(low) : 0.f);
+          const bool may = ki > kNone && !(of_key(ki) < low - (a.bias ? slack + 4.f * unit * fabsf(low) : 0.f));   // also at low = inf
           if (__any_sync(kFull, may) && may) {
             const unsigned long long x =
                 exact_choice(a.sigmoid, logit_at<E>(a, t, e0 + i), a.bias ? a.bias[e0 + i] : 0.f, (double)m, den64);

@@ -520,8 +520,9 @@ typedef struct {
  *           expert index);  topk_w = score[topk_ids] (/ their sum) * scale
  * The bias decides the selection only; the weights come from the scores.
  * The ids are those that 64-bit arithmetic gives: where two choices (or two
- * groups) lie closer than the error of the FP32 scores, the row is redone in
- * FP64.  A logit of -inf or NaN masks its expert: no score, never eligible; a
+ * groups) lie closer than the error of the FP32 scores, they are redone in
+ * FP64.  Different logits whose 64-bit scores are equal (sigmoids of 38 and 50
+ * are both 1) tie, with or without a bias.  A logit of -inf or NaN masks its expert: no score, never eligible; a
  * bias of -inf or NaN takes the expert out of the selection, not out of the
  * softmax.  A group's value counts its eligible choices (one, if it has only
  * one); a group without any is last.  A row with fewer than k eligible

@@ -1,5 +1,6 @@
 """route_scored at the ends of its arithmetic, ids against the float64 oracle:
-group sums of choices that cancel or overflow."""
+group sums of choices that cancel or overflow, scores that are equal though
+their logits differ."""
 import pytest
 import torch
 
@@ -47,3 +48,39 @@ def test_group_sums_that_overflow(score, per):
         alone = bias.clone().view(groups, per)
         alone[::2, 1:] = -INF   # one choice, or two
         check_route(logits, alone.view(-1), 1, score=score, groups=groups, top_groups=2, group_rank=2)
+
+
+# Logits whose 64-bit scores are equal although the logits differ: sigmoids that
+# round to 1, softmax terms below the smallest number, values far below 1.
+SATURATED = {"sigmoid": (60.0, 50.0, 45.0, 40.0, 38.0, 20.0, 2.0, -3.0, INF),
+             "softmax": (0.0, -750.0, -800.0, -900.0, -2000.0, -3e38, -1.0, 1e-20, -1e-25)}
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups", [(4, 2, 1), (32, 6, 4), (60, 5, 6), (64, 8, 8), (64, 8, 1), (256, 8, 8),
+                                        (300, 10, 1)])
+def test_saturated_scores_tie(score, E, k, groups):
+    """Equal 64-bit scores go to the lower index, with and without a bias."""
+    T = 256
+    g = torch.Generator().manual_seed(E + k)
+    vals = torch.tensor(SATURATED[score])
+    logits = vals[torch.randint(0, len(vals), (T, E), generator=g)]
+    logits[::4] = torch.where(torch.rand(T // 4, E, generator=g) < 0.8, torch.randn(T // 4, E, generator=g), logits[::4])
+    if score == "softmax":
+        logits[1::16, 0] = 0.0      # so that the rest underflows
+        logits[1::16, 1:] = logits[1::16, 1:].clamp_max(-750)
+        logits[2::16, E // 2] = INF
+    logits = logits.cuda()
+    for top in (1,) if groups == 1 else (1, groups // 2):
+        for rank in (1, 2):
+            if k > top * (E // groups):
+                continue
+            kw = dict(score=score, groups=groups, top_groups=top, group_rank=rank)
+            ids, _ = check_route(logits, None, k, **kw)
+            assert torch.equal(ids, check_route(logits, torch.zeros(E, device="cuda"), k, **kw)[0])
+
+
+def test_saturated_scores_by_hand():
+    logits = torch.tensor([[40.0, 50.0, 1.0, 2.0], [50.0, 2.0, 40.0, 45.0]], device="cuda")
+    assert check_route(logits, None, 2, score="sigmoid")[0].tolist() == [[0, 1], [0, 2]]
+    assert check_route(logits, None, 1, score="sigmoid", groups=2, top_groups=1)[0].tolist() == [[0], [0]]

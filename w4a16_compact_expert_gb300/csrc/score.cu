@@ -19,9 +19,10 @@
 // only the experts at the border are taken up again in FP64, one per lane: a
 // whole token in FP64 takes a warp 16 us of dependent operations (when every
 // close token went that way, T = 2048, E = 256 with groups took 13.5 us).
-// With no bias the experts are ordered by the logits themselves (both scores
-// are increasing in them), which is exact, so only group values (sums of two
-// scores) need the check.
+// With no bias the FP32 pass orders the experts by the logits themselves (both
+// scores are increasing in them), which is exact but for logits whose 64-bit
+// scores are equal (sigmoids that round to 1, softmax terms that underflow):
+// these tie, so borders between them are close ones too.
 #include "block.h"
 
 namespace {
@@ -80,12 +81,19 @@ DEV_INLINE float score_of(const ScoreArgs& a, float l, float m, float den) {
   return __fdividef(l == m ? 1.f : expf(l - m), den);
 }
 
-// The FP64 choice of one expert, as a key; m and den: the softmax's.
+// The FP64 score of a logit that is not masked; m and den: the softmax's.  One
+// copy of exp for both scores; a sigmoid below e^-700 is e^l, where e^-l would
+// overflow.
+DEV_INLINE double exact_score(bool sigmoid, double l, double m, double den) {
+  const bool low = l < -700.0;
+  const double x = exp(!sigmoid ? l - m : low ? l : -l);
+  return !sigmoid ? (l == m ? 1.0 : x) / den : low ? x : 1.0 / (1.0 + x);
+}
+
+// The FP64 choice of one expert, as a key.
 __device__ __noinline__ unsigned long long exact_choice(bool sigmoid, float l, float b, double m, double den) {
   if (l == -INFINITY || !(b > -INFINITY)) return kNone64;
-  const double x = exp(sigmoid ? -(double)l : (double)l - m);
-  const double s = sigmoid ? 1.0 / (1.0 + x) : ((double)l == m ? 1.0 : x) / den;
-  return key_of(s + (double)b);
+  return key_of(exact_score(sigmoid, (double)l, m, den) + (double)b);
 }
 
 template <typename E>
@@ -121,20 +129,13 @@ __device__ __noinline__ void choose_exact(const ScoreArgs& a, long long t, unsig
 #pragma unroll 1
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
   }
-  auto score = [&](double l) -> double {   // one copy of exp for both scores
-    if (l == -INFINITY) return 0.0;
-    const double x = exp(a.sigmoid ? -l : l - m);
-    return a.sigmoid ? 1.0 / (1.0 + x) : (l == m ? 1.0 : x) / den;
-  };
-  const bool grouped = a.G > 1, scored = a.bias || (grouped && a.two);
+  auto score = [&](double l) -> double { return l == -INFINITY ? 0.0 : exact_score(a.sigmoid, l, m, den); };
+  const bool grouped = a.G > 1;
 #pragma unroll 1
   for (int e = lane; e < a.E; e += 32) {
     const double l = logit_at<E>(a, t, e);
     const float b = a.bias ? a.bias[e] : 0.f;
-    double c = l;
-    if (l == -INFINITY || !(b > -INFINITY)) c = -INFINITY;
-    else if (scored) c = score(l) + (double)b;
-    cell[e] = key_of(c);
+    cell[e] = l == -INFINITY || !(b > -INFINITY) ? kNone64 : key_of(score(l) + (double)b);
   }
   __syncwarp();
   if (grouped) {
@@ -165,12 +166,9 @@ __device__ __noinline__ void choose_exact(const ScoreArgs& a, long long t, unsig
       rank += ov > gv || (ov == gv && o < g);
     }
     const unsigned kept = __ballot_sync(kFull, g < a.G && rank < a.top_groups);
-    // with no bias the logits order the experts of the kept groups
 #pragma unroll 1
-    for (int e = lane; e < a.E; e += 32) {
+    for (int e = lane; e < a.E; e += 32)
       if (!((kept >> ((e / a.per) * L)) & 1u)) cell[e] = kNone64;
-      else if (!a.bias) cell[e] = key_of((double)logit_at<E>(a, t, e));
-    }
     __syncwarp();
   }
   unsigned long long mine = 0;
@@ -254,7 +252,8 @@ DEV_INLINE void load_logits(const ScoreArgs& a, long long t, float (&l)[EPL]) {
 
 // True, with nothing written, where the token has to be done in FP64 as a whole:
 // a close border between groups that do not lie on whole lanes, more close
-// experts than lanes, or scores that FP32 cannot hold.
+// experts than lanes, scores that FP32 cannot hold, or logits that differ where
+// their scores may not.
 template <typename E, int EPL>
 DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
   const int lane = threadIdx.x & 31, e0 = lane * EPL;
@@ -298,6 +297,20 @@ DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
     }
     key[i] = e0 + i < a.E ? key_of(c) : 0u;
   }
+  // With no bias: may the 64-bit scores of two logits c0 > c1 be equal (or come
+  // out the other way round)?  Where their relative difference (softmax: c0 -
+  // c1; sigmoid: (c0 - c1)(1 - score), or more than half of it) comes near the
+  // roundings of FP64, some 2^-51 of 1 (softmax: of 1 + |l - m|), or the terms
+  // leave its range.  `suspect` sees from c0 alone that it is not so: FP32
+  // logits that differ lie farther apart.
+  auto suspect = [&](float c0) -> bool {
+    return fabsf(c0) < 1e-4f || (a.sigmoid ? c0 > 16.f || c0 < -700.f : m - c0 > 700.f);
+  };
+  auto saturated = [&](float c0, float c1) -> bool {
+    const float rel = a.sigmoid ? fminf(c0 - c1, 1.f) * blk::fast_rcp(1.f + blk::fast_exp(c1))
+                                : (c0 - c1) * blk::fast_rcp(1.f + (m - c1));
+    return c0 > c1 && (rel <= 1.4e-14f || (a.sigmoid ? 0.f : m) - c0 > 700.f);
+  };
   double den64 = -1.0;   // the softmax denominator in FP64, once asked for
   uint32_t srt[EPL];
 #pragma unroll
@@ -336,22 +349,27 @@ DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
       b2 = max(min(b1, o1), max(b2, o2));
       b1 = max(b1, o1);
     }
-    // The group's value and a bound of its FP32 error: half of `slack` for each
-    // choice's score, and the roundings of the choices and of their sum, a unit
-    // each and taken twice, which count by the choices' own size: of opposite
-    // sign they may cancel.  With an eligible expert the value is never -inf,
-    // also where the sum overflows.
-    float gv = of_key(max(b1, kNone)), err = 0.5f * slack + 4.f * unit * fabsf(gv);
-    if (a.two) {
-      float v2 = of_key(max(b2, kNone));
-      if (!a.bias && gv != -INFINITY) {   // keys of logits: their scores
+    // What ranks the groups: logits, or half their value (so that no sum
+    // overflows; an infinite bias counts as the largest number) with a bound of
+    // its FP32 error: half of `slack` for each choice's score, and the roundings
+    // of the choices and of their sum, a unit each and taken twice, which count
+    // by the choices' own size: of opposite sign they may cancel.
+    const float largest = 3.402823466e38f;
+    float gv = of_key(max(b1, kNone)), err = 0.f;
+    const bool none = gv == -INFINITY;
+    if (scored) {
+      float v2 = a.two ? of_key(max(b2, kNone)) : -INFINITY;
+      if (!a.bias && !none) {   // keys of logits: their scores
         gv = score_of(a, gv, m, den);
         if (v2 != -INFINITY) v2 = score_of(a, v2, m, den);
       }
-      err = 0.5f * slack + 4.f * unit * fabsf(gv);
+      gv = fminf(gv, largest);
+      err = 0.25f * slack + 2.f * unit * fminf(fabsf(gv), largest);
+      gv *= 0.5f;
       if (v2 != -INFINITY) {
-        err += 0.5f * slack + 4.f * unit * fabsf(v2);
-        gv = fmaxf(gv + v2, -3.402823466e38f);
+        v2 = fminf(v2, largest);
+        err += 0.25f * slack + 2.f * unit * fabsf(v2);
+        gv += 0.5f * v2;
       }
     }
     int rank = 0;   // how many groups come before
@@ -363,15 +381,14 @@ DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
     if (scored) {
       // the 64-bit value lies between lo and hi; a kept group that may lie below
       // a dropped one makes the border a close one
-      const bool none = gv == -INFINITY, sure = fabsf(gv) < 3.402823466e38f && err < INFINITY;
-      const float lo = sure ? gv - err : none ? gv : -3.402823466e38f, hi = sure ? gv + err : none ? gv : INFINITY;
+      const float lo = gv - err, hi = gv + err;
       const float least = -warp_max_f(kept ? -lo : -INFINITY), most = warp_max_f(g < a.G && !kept ? hi : -INFINITY);
       if (most != -INFINITY && least <= most) {   // the same in every lane
         if (!whole) return true;
         // the groups on either side of the border in FP64, from their experts
         // that may be among the largest
         if (!a.sigmoid && den64 < 0.0) den64 = exact_den<E>(a, t, (double)m);
-        const bool border = g < a.G && gv != -INFINITY && (kept ? lo <= most : hi >= least);
+        const bool border = g < a.G && !none && (kept ? lo <= most : hi >= least);
         const float low = of_key(max(a.two ? b2 : b1, kNone));
         unsigned long long x1 = 0ull, x2 = 0ull;
         for (int i = 0; i < EPL; ++i) {
@@ -389,7 +406,7 @@ DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
           x2 = max(min(x1, o1), max(x2, o2));
           x1 = max(x1, o1);
         }
-        const unsigned long long gx = !border ? key_of((double)gv)
+        const unsigned long long gx = !border ? key_of(2.0 * (double)gv)
                                       : a.two && x2 > kNone64 ? key_of(of_key(x1) + of_key(x2)) : x1;
         rank = 0;
         for (int o = 0; o < a.G; ++o) {
@@ -398,6 +415,10 @@ DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
         }
         kept = g < a.G && rank < a.top_groups;
       }
+    } else if (__any_sync(kFull, kept && !none && suspect(gv))) {
+      const float least = -warp_max_f(kept ? -gv : -INFINITY), most = warp_max_f(g < a.G && !kept ? gv : -INFINITY);
+      if (__any_sync(kFull, g < a.G && !none && most != -INFINITY && (kept ? saturated(gv, most) : saturated(least, gv))))
+        return true;
     }
     const unsigned kb = __ballot_sync(kFull, kept);
     // the experts of dropped groups are not eligible
@@ -495,6 +516,17 @@ DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
         chosen = cell[lane] >> 31;
       }
     }
+  } else if (__any_sync(kFull, chosen && suspect(of_key(mine)))) {
+    const float c = of_key(max(mine, kNone)), next = __shfl_down_sync(kFull, c, 1), kc = __shfl_sync(kFull, c, a.k - 1);
+    float rest = -INFINITY;   // of this lane's others the largest below the last chosen (at equal ones the index decided)
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float v = of_key(max(srt[i], kNone));
+      if (v < kc) rest = fmaxf(rest, v);
+    }
+    if (__any_sync(kFull, (lane + 1 < a.k && next != -INFINITY && saturated(c, next)) ||
+                              (rest != -INFINITY && saturated(kc, rest))))
+      return true;
   }
   const float my_l = chosen ? logit_at<E>(a, t, my_e) : -INFINITY;
   float w = 0.f;

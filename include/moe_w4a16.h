@@ -168,9 +168,9 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_forward(moe_w4a16_handle* h, const void
  * with y as in moe_w4a16_forward and the ranks summed in j order in FP32.
  *   topk_ids [T][k] int32, topk_w [T][k] FP32: device, k = the handle's top_k;
  *   an id may occur more than once in a row.
- * Flags: RESIDUAL, FORCE_GEMV, FORCE_GEMM.  An absent expert contributes 0 and
- * counts as a miss; an id outside [0, E) counts as a miss too and is taken as
- * expert 0 with weight 0.  Runs as separate launches in every regime (1 or 3
+ * Flags: RESIDUAL, FORCE_GEMV, FORCE_GEMM.  A pair whose weight is 0, whose
+ * expert is absent or whose id lies outside [0, E) contributes exactly nothing,
+ * whatever the expert's output; each of the latter two counts as a miss.  Runs as separate launches in every regime (1 or 3
  * for the permutation, then the decode kernels or the grouped GEMM; see
  * moe_w4a16_last_path); everything else as for moe_w4a16_forward. */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_forward_routed(moe_w4a16_handle* h, const void* x, int32_t T,

@@ -174,3 +174,48 @@ def test_block(T, bits, score, bias):
         assert m.get_status() == (F.OK, 0) and B.status() == F.OK
     finally:
         m.close()
+
+
+@pytest.mark.parametrize("T,force", [(1, F.FORCE_GEMV), (4, F.FORCE_GEMV), (12, F.FORCE_GEMV), (4, F.FORCE_GEMM),
+                                     (90, F.FORCE_GEMM)])
+def test_routed_bad_ids_contribute_exactly_nothing(T, force):
+    """Also where expert 0's output is not finite, or expert 0 is absent (each bad id is one miss)."""
+    layer = synth.make_layer(synth.TINY, 79)
+    rng = np.random.default_rng(T)
+    x = synth.draw_x(9, T, 256)
+    ids = rng.integers(1, 8, (T, 2)).astype(np.int32)
+    ids[::2, 1] = np.array([-1, 8, 2 ** 31 - 1, -2 ** 31])[np.arange((T + 1) // 2) % 4]
+    w = rng.standard_normal((T, 2)).astype(np.float32)
+    bad = int(((ids < 0) | (ids > 7)).sum())
+    ref = oracle_routed(layer, x, ids, w)
+    m = F.MoELayer(256, 128, 8, 2, num_slots=8, max_tokens=T)
+    try:
+        gq, gs, uq, us, dq, ds = (a.copy() for a in layer.slot_experts().arrays())
+        us[0] = 0x7E00   # NaN
+        m.pack_experts(0, gq, gs, uq, us, dq, ds)
+        for absent in (False, True):
+            m.set_slot_table(np.array([-1 if absent else 0, 1, 2, 3, 4, 5, 6, 7], np.int32))
+            out = m.forward_routed(gp.to_dev(x), gp.to_dev(ids), gp.to_dev(w), force)
+            assert m.get_status() == (F.ERR_NOT_RESIDENT, bad)
+            gp.assert_output(out.float().cpu().numpy().astype(np.float64), ref, np.ones(T, bool))
+    finally:
+        m.close()
+
+
+@pytest.mark.parametrize("force", [F.FORCE_GEMV, F.FORCE_GEMM])
+def test_routed_weight_zero_contributes_exactly_nothing(force):
+    layer = synth.make_layer(synth.TINY, 80)
+    x = synth.draw_x(9, 6, 256)
+    ids = np.array([[0, 3]] * 6, np.int32)
+    w = np.array([[0.0, 0.5], [-0.0, 1.0]] * 3, np.float32)
+    m = F.MoELayer(256, 128, 8, 2, num_slots=8, max_tokens=6)
+    try:
+        gq, gs, uq, us, dq, ds = (a.copy() for a in layer.slot_experts().arrays())
+        us[0] = 0x7E00   # NaN
+        m.pack_experts(0, gq, gs, uq, us, dq, ds)
+        m.set_slot_table(layer.expert_to_slot)
+        out = m.forward_routed(gp.to_dev(x), gp.to_dev(ids), gp.to_dev(w), force)
+        assert m.get_status() == (F.OK, 0)
+        gp.assert_output(out.float().cpu().numpy().astype(np.float64), oracle_routed(layer, x, ids, w), np.ones(6, bool))
+    finally:
+        m.close()

@@ -518,6 +518,7 @@ moe_w4a16_status moe_w4a16_forward_routed(moe_w4a16_handle* h, const void* x, in
   if ((long long)T * c.k < ma) ma = T * c.k;
   if (h->cfg.num_slots < ma) ma = h->cfg.num_slots;
   c.max_active = ma;
+  c.given = 1;
   cudaError_t e = record_stage(h->events, 0, st);
   if (e == cudaSuccess) e = launch_route_given(c, topk_ids, topk_w, st);
   if (e == cudaSuccess && !gemm) e = record_stage(h->events, 1, st);   // the GEMM family records it after the gather

@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(256) gemv_down_kernel(FwdCtx c, int hrows) {
     float acc = residual ? __half2float(c.x[(size_t)t * H + hrow]) : 0.f;
     for (int j = 0; j < c.k; ++j) {
       const int p = t * c.k + j;
-      if (c.table[c.ids[p]] >= 0) acc = fmaf(c.topw[p], __ldcg(&c.ybuf[(size_t)p * H + hrow]), acc);
+      if (c.table[c.ids[p]] < 0 || (c.given && c.topw[p] == 0.f)) continue;   // the grouped GEMM's combine skips weights of 0 too
+      acc = fmaf(c.topw[p], __ldcg(&c.ybuf[(size_t)p * H + hrow]), acc);
     }
     c.out[(size_t)t * H + hrow] = __float2half_rn(acc);
   }

@@ -53,6 +53,7 @@ struct FwdCtx {
   DevStatus* status;
   int num_sms;
   int max_active;              // upper bound of active experts: min(E, T*k)
+  int given;                   // routing given by the caller: a pair of weight 0 contributes nothing
   // offload-qpacked comparison path: FP16 execution slots
   __half* xpool;               // [xslots][gate I*H | up I*H | down H*I], row-major, K contiguous
   uint64_t xslot_halves;       // halves per execution slot (3 I H)

@@ -675,16 +675,19 @@ __global__ void __launch_bounds__(256) route_coop_kernel(FwdCtx c) {
 
 // ------------------------------------------------- routing given by the caller
 // Copies the caller's ids and weights into the handle's routing buffers.  An id
-// outside [0, E) becomes expert 0 with weight 0 and counts as a miss, so that
-// no index leaves its array.
+// outside [0, E) becomes expert 0 with weight 0, which contributes nothing, so
+// that no index leaves its array; it counts as one miss (where expert 0 is
+// absent, the permutation counts it).
 DEV_INLINE int take_given(const FwdCtx& c, const int32_t* ids, const float* w, int p) {
   int e = ids[p];
   float v = w[p];
   if ((unsigned)e >= (unsigned)c.E) {
     e = 0;
     v = 0.f;
-    atomicAdd(&c.status->miss, 1ull);
-    atomicOr(&c.status->flags, STATUS_MISS);
+    if (c.table[0] >= 0) {
+      atomicAdd(&c.status->miss, 1ull);
+      atomicOr(&c.status->flags, STATUS_MISS);
+    }
   }
   c.ids[p] = e;
   c.topw[p] = v;

@@ -146,3 +146,17 @@ def test_oracle_linear_by_hand():
     assert np.allclose(out, [[-2 * 3 / (1 + math.exp(-3))]])
     out, *_ = O.linear(x, w, x_scale=np.array([2.0]), w_scale=np.array([1.0, 3.0]))
     assert out.tolist() == [[6.0, -12.0]]
+
+
+def test_no_copy_is_shared_over_a_cluster():
+    """Every copy loads into one CTA: the library also runs as one of several replicas on a machine, on any device memory."""
+    import glob
+    import os
+    import re
+    sources = [f for e in ("cu", "cuh", "h", "cpp") for f in glob.glob(os.path.join(build_ext.CSRC, "*." + e))]
+    assert len(sources) > 10
+    for path in sources:
+        with open(path) as f:
+            text = re.sub(r'"\s*\n\s*"', "", f.read())   # joined string literals
+        for stmt in re.findall(r"cp\.async\.bulk[^;]*", text):
+            assert "multi" + "cast" not in stmt, (os.path.basename(path), stmt)

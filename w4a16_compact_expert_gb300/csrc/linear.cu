@@ -129,7 +129,7 @@ DEV_INLINE void umma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t
 }
 
 // Arrives on `bar` once the MMAs issued so far are done; the pair form at its
-// place in every CTA of the mask.
+// place in both CTAs.
 DEV_INLINE void commit_one(uint64_t* bar, uint32_t leader) {
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
@@ -137,12 +137,12 @@ DEV_INLINE void commit_one(uint64_t* bar, uint32_t leader) {
       "r"(leader)
       : "memory");
 }
-DEV_INLINE void commit_pair(uint64_t* bar, uint32_t mask, uint32_t leader) {
+DEV_INLINE void commit_pair(uint64_t* bar, uint32_t leader) {
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
       " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)mask), "r"(leader)
+      "h"((uint16_t)3), "r"(leader)
       : "memory");
 }
 
@@ -172,18 +172,6 @@ DEV_INLINE void fetch(uint32_t dst, const CUtensorMap* tmap, int c0, int r0, uin
         " [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
         "l"(tmap), "r"(c0), "r"(r0), "r"(bar), "r"(leader)
         : "memory");
-}
-
-// TMA box -> the same place in every CTA of the mask; each counts it at the
-// barrier of its pair's first CTA (`bar` is the address in such a CTA).
-DEV_INLINE void fetch_shared(uint32_t dst, const CUtensorMap* tmap, int c0, int r0, uint32_t bar, uint32_t mask,
-                             uint32_t leader) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %6, 0;\n"
-      " @q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      ".cta_group::2 [%0], [%1, {%2, %3}], [%4], %5;\n}\n" ::"r"(dst),
-      "l"(tmap), "r"(c0), "r"(r0), "r"(bar), "h"((uint16_t)mask), "r"(leader)
-      : "memory");
 }
 
 // Starts a box on its way into the L2 cache.  Allowed before the grids ahead
@@ -551,11 +539,7 @@ __global__ void __launch_bounds__(192, 2)
 // -------------------------------------------------------------------- wide
 // A pair of CTAs shares one tile of 256 tokens x BN weight rows: each loads
 // its 128 token rows and half of the weight rows, the first issues the MMAs of
-// both, and each finishes its 128 tokens.  PAIRS = 2: two pairs with
-// neighbouring weight tiles form a cluster and share their token rows: each CTA
-// loads half of its 128 rows for itself and its counterpart (TMA multicast).
-// That saves a quarter of a 256-row tile's reads from the L2, a third of a
-// 128-row tile's.
+// both, and each finishes its 128 tokens.
 template <int BN>
 struct WideCfg {
   static constexpr int kA = 128 * kChunk;   // the 128 token rows of this CTA
@@ -631,7 +615,7 @@ DEV_INLINE void finish_turned(const LinearArgs& a, const float* buf, int t0, int
   store_quads<O, kPass>(a, t, live, n0 + c, step, v);
 }
 
-template <bool F8, bool GATED, int BN, int PAIRS, typename O>
+template <bool F8, bool GATED, int BN, typename O>
 __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     linear_wide_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmX) {
@@ -648,14 +632,10 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
   uint64_t* acc_empty = acc_full + 2;        // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int crank = (int)cluster_rank(), rank = crank & 1, pair = crank >> 1;   // rank: in the pair
-  const int mtiles = (a.T + 255) / 256;
-  // a unit of work: the tile of each of the cluster's pairs; with an odd number
-  // of weight tiles the last unit's second tile is empty (zeros, not stored)
-  const int tiles = mtiles * ((a.N + FT * PAIRS - 1) / (FT * PAIRS));
+  const int rank = (int)cluster_rank();
+  const int mtiles = (a.T + 255) / 256, tiles = mtiles * ((a.N + FT - 1) / FT);
   const int nk = (a.K + kElem - 1) / kElem;
-  const int first = blockIdx.x / (2 * PAIRS), step = gridDim.x / (2 * PAIRS);
-  const uint32_t pair_mask = 3u << (crank & ~1), all_mask = (1u << (2 * PAIRS)) - 1u;
+  const int first = blockIdx.x / 2, step = gridDim.x / 2;
 
   if (threadIdx.x == 32) {
     prefetch_map(&tmW);
@@ -664,7 +644,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], PAIRS);   // every pair that reads this CTA's loads
+      mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&acc_full[s], 1);
@@ -690,9 +670,9 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     Pipe p;
     bool ok = true;
     int issued = 0;
-    const uint32_t leader = elect_lane(), ring = smem_u32(smem), bars = smem_u32(full), bars0 = map_to_rank(full, crank & ~1);
+    const uint32_t leader = elect_lane(), ring = smem_u32(smem), bars = smem_u32(full), bars0 = map_to_rank(full, 0);
     for (int tile = first; tile < tiles && ok; tile += step) {
-      const int m0 = (tile % mtiles) * 256 + rank * 128, n0 = (tile / mtiles * PAIRS + pair) * FT;
+      const int m0 = (tile % mtiles) * 256 + rank * 128, n0 = tile / mtiles * FT;
       const int b0 = rank == 0 ? n0 : GATED ? a.N + n0 : n0 + BN / 2;   // this CTA's weight rows
       for (int k = 0; k < nk; ++k) {
         if (!mbar_wait_bounded(&empty[p.i], p.ph ^ 1u, &g_block_status)) {
@@ -701,10 +681,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
         }
         const uint32_t dst = ring + (uint32_t)(p.i * C::kStage), bar0 = bars0 + (uint32_t)(p.i * 8);
         if (rank == 0) expect_bytes(bars + (uint32_t)(p.i * 8), (uint32_t)(2 * C::kStage), leader);
-        if constexpr (PAIRS == 1)
-          fetch<2>(dst, &tmX, k * kElem, m0, bar0, leader);
-        else   // rows 64 pair .. + 63 of the 128, for both pairs' CTAs of this rank
-          fetch_shared(dst + pair * (C::kA / 2), &tmX, k * kElem, m0 + pair * 64, bar0, 5u << rank, leader);
+        fetch<2>(dst, &tmX, k * kElem, m0, bar0, leader);
         fetch<2>(dst + C::kA, &tmW, k * kElem, b0, bar0, leader);
         ++issued;
         p.next(C::kStages);
@@ -739,10 +716,10 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             umma<F8, 2>(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (uint32_t)((k | j) != 0), leader);
-          commit_pair(&empty[p.i], all_mask, leader);
+          commit_pair(&empty[p.i], leader);
           p.next(C::kStages);
         }
-        if (ok) commit_pair(&acc_full[acc.i], pair_mask, leader);
+        if (ok) commit_pair(&acc_full[acc.i], leader);
         acc.next(2);
       }
     }
@@ -754,7 +731,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     float* buf = turn + (warp - 2) * (C::kTurn / 4);
     Pipe acc;
     for (int tile = first; tile < tiles; tile += step) {
-      const int t0 = (tile % mtiles) * 256 + rank * 128 + q * 32, n0 = (tile / mtiles * PAIRS + pair) * FT;
+      const int t0 = (tile % mtiles) * 256 + rank * 128 + q * 32, n0 = tile / mtiles * FT;
       constexpr int kStep = GATED ? 16 : 32, kLanes = kStep / 4, kPart = FT / C::kParts;
       // Under the tile's MMAs: this warp's part of the residual starts towards
       // the L2 (a lane takes a row), and its rows' scales (one to a lane) and its
@@ -817,7 +794,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
       __syncwarp();
       if (lane == 0)
         asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                         map_to_rank(&acc_empty[acc.i], crank & ~1))
+                         map_to_rank(&acc_empty[acc.i], 0))
                      : "memory");
       acc.next(2);
     }
@@ -957,35 +934,35 @@ cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
                     prefetch);
 }
 
-template <bool F8, bool GATED, int BN, int PAIRS, typename O>
+template <bool F8, bool GATED, int BN, typename O>
 cudaError_t launch_wide_o(const Problem& p, cudaStream_t st) {
   using C = WideCfg<BN>;
   CUtensorMap mw, mx;
   if (!encode_rows(&mw, p.w, GATED ? 2ll * p.a.N : p.a.N, p.a.K, p.elem, p.ld_w, BN / 2) ||
-      !encode_rows(&mx, p.x, p.a.T, p.a.K, p.elem, p.ld_x, 128 / PAIRS))
+      !encode_rows(&mx, p.x, p.a.T, p.a.K, p.elem, p.ld_x, 128))
     return cudaErrorInvalidValue;
-  auto kernel = linear_wide_kernel<F8, GATED, BN, PAIRS, O>;
+  auto kernel = linear_wide_kernel<F8, GATED, BN, O>;
   cudaError_t e = opt_in_smem((const void*)kernel, C::kSmem);
   if (e != cudaSuccess) return e;
   static std::atomic<int> resident[kMaxDevices];   // clusters that run at once, asked once per device
   int n = resident[p.dev].load(std::memory_order_relaxed);
   if (!n) {
-    e = active_clusters(C::kThreads, C::kSmem, 2 * PAIRS, &n);
+    e = active_clusters(C::kThreads, C::kSmem, 2, &n);
     if (e != cudaSuccess) return e;
     resident[p.dev].store(n, std::memory_order_relaxed);
   }
-  const int FT = (GATED ? BN / 2 : BN) * PAIRS;
-  const long long units = (long long)((p.a.T + 255) / 256) * ((p.a.N + FT - 1) / FT);
-  if (units > 0x1fffffff) return cudaErrorInvalidConfiguration;
-  return launch_pdl(kernel, dim3((unsigned)((units < n ? units : n) * 2 * PAIRS)), dim3(C::kThreads), C::kSmem, st,
-                    2 * PAIRS, p.a, mw, mx);
+  constexpr int FT = GATED ? BN / 2 : BN;
+  const long long tiles = (long long)((p.a.T + 255) / 256) * ((p.a.N + FT - 1) / FT);
+  if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
+  return launch_pdl(kernel, dim3((unsigned)((tiles < n ? tiles : n) * 2)), dim3(C::kThreads), C::kSmem, st, 2, p.a, mw,
+                    mx);
 }
 
-template <bool F8, bool GATED, int BN, int PAIRS>
+template <bool F8, bool GATED, int BN>
 cudaError_t launch_wide(const Problem& p, cudaStream_t st) {
-  return p.out_dtype == MOE_W4A16_F16    ? launch_wide_o<F8, GATED, BN, PAIRS, __half>(p, st)
-         : p.out_dtype == MOE_W4A16_BF16 ? launch_wide_o<F8, GATED, BN, PAIRS, __nv_bfloat16>(p, st)
-                                         : launch_wide_o<F8, GATED, BN, PAIRS, float>(p, st);
+  return p.out_dtype == MOE_W4A16_F16    ? launch_wide_o<F8, GATED, BN, __half>(p, st)
+         : p.out_dtype == MOE_W4A16_BF16 ? launch_wide_o<F8, GATED, BN, __nv_bfloat16>(p, st)
+                                         : launch_wide_o<F8, GATED, BN, float>(p, st);
 }
 
 // The tile width of the wide kernel: rounds of tiles over the resident
@@ -995,30 +972,22 @@ cudaError_t launch_wide(const Problem& p, cudaStream_t st) {
 // of 5 ns.  Measured at N = K = 2048 with 256 / 128 / 64 rows: T = 512 14.2 /
 // 9.0 / 8.2 us, T = 1024 14.5 / 10.1 / 12.8, T = 4096 24.6 / 26.3 / 36.0.
 template <bool GATED>
-int wide_rows(const Problem& p, int pairs) {
+int wide_rows(const Problem& p) {
   const long long nk = (p.a.K + kChunk / p.elem - 1) / (kChunk / p.elem);
-  const long long slots = pairs == 1 ? p.num_sms / 2 : p.num_sms * 9 / 38;   // of 152 SMs: 76 pairs, 36 clusters of two
+  const long long slots = p.num_sms / 2;
   const int rows[3] = {256, 128, 64}, chunk[3] = {58, 34, 28}, fixed[3] = {520, 340, 240};
   int best = 0;
   long long cost = -1;
   for (int i = 0; i < 3; ++i) {
-    const int ft = (GATED ? rows[i] / 2 : rows[i]) * pairs;
-    const long long units = (long long)((p.a.T + 255) / 256) * ((p.a.N + ft - 1) / ft);
-    const long long c = (units + slots - 1) / slots * nk * chunk[i] + fixed[i];
+    const int ft = GATED ? rows[i] / 2 : rows[i];
+    const long long tiles = (long long)((p.a.T + 255) / 256) * ((p.a.N + ft - 1) / ft);
+    const long long c = (tiles + slots - 1) / slots * nk * chunk[i] + fixed[i];
     if (cost < 0 || c < cost) {
       cost = c;
       best = rows[i];
     }
   }
   return best;
-}
-
-template <bool F8, bool GATED, int PAIRS>
-cudaError_t launch_wide_rows(const Problem& p, cudaStream_t st) {
-  const int rows = wide_rows<GATED>(p, PAIRS);
-  return rows == 256   ? launch_wide<F8, GATED, 256, PAIRS>(p, st)
-         : rows == 128 ? launch_wide<F8, GATED, 128, PAIRS>(p, st)
-                       : launch_wide<F8, GATED, 64, PAIRS>(p, st);
 }
 
 // Up to 64 tokens the narrow kernel (N = K = 2048: T = 64 5.5 us, the wide one
@@ -1028,13 +997,10 @@ cudaError_t launch_gated(const Problem& p, cudaStream_t st) {
   if (p.a.T <= 16) return launch_narrow<F8, GATED, 16>(p, st);
   if (p.a.T <= 32) return launch_narrow<F8, GATED, 32>(p, st);
   if (p.a.T <= 64) return launch_narrow<F8, GATED, 64>(p, st);
-  // Two pairs to a cluster where rows do not start on 128-byte lines: each box
-  // row then touches two lines and up to five sectors, the L2 sets the pace,
-  // and sharing the tokens helps (K = 1416, N = 4000 FP16: T = 333 12.0 -> 9.0
-  // us, T = 4096 42.6 -> 35.1).  On lines it does not (K = 2048, N = 2048, T =
-  // 4096 24.6 and 24.6), and fewer SMs fit the larger clusters.
-  const bool lines = p.ld_x % 128 == 0 && p.ld_w % 128 == 0;
-  return lines ? launch_wide_rows<F8, GATED, 1>(p, st) : launch_wide_rows<F8, GATED, 2>(p, st);
+  const int rows = wide_rows<GATED>(p);
+  return rows == 256   ? launch_wide<F8, GATED, 256>(p, st)
+         : rows == 128 ? launch_wide<F8, GATED, 128>(p, st)
+                       : launch_wide<F8, GATED, 64>(p, st);
 }
 
 template <bool F8>

@@ -570,8 +570,20 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linear_config* c
 
 /* Synchronises the calling thread's current device, reads and clears the
  * status word of the block operators there: OK, or ERR_TIMEOUT if a bounded
- * wait of moe_w4a16_linear gave up since the last call. */
+ * wait of moe_w4a16_linear gave up since the last call (the outputs of that
+ * call are then not valid). */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_block_status(void);
+
+/* Failure-detection self-test of moe_w4a16_linear, without a fault: the same
+ * call (F16 in and out, no activation; T in [1, 16] or above 64) in which
+ * which = 0 the multiplying warps, 1 the loading warps, 2 every other loading
+ * warp stop after two K chunks, so that bounded waits, here of limit_cycles SM
+ * cycles (1000..2^31), run out.  The kernel returns within some seconds, out
+ * holds nothing of use, and moe_w4a16_block_status reports ERR_TIMEOUT.  K is
+ * to be large enough that CTAs have more than two chunks. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_selftest_linear(const moe_w4a16_linear_config* cfg, int64_t T, const void* x,
+                                                         const void* w, void* out, int32_t which,
+                                                         int64_t limit_cycles, moe_w4a16_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -160,3 +160,16 @@ def test_no_copy_is_shared_over_a_cluster():
             text = re.sub(r'"\s*\n\s*"', "", f.read())   # joined string literals
         for stmt in re.findall(r"cp\.async\.bulk[^;]*", text):
             assert "multi" + "cast" not in stmt, (os.path.basename(path), stmt)
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(in_dtype=1), "F16"), (dict(out_dtype=2), "F16"), (dict(act=1), "F16"), (dict(T=0), "T outside"),
+    (dict(T=17), "T outside"), (dict(T=64), "T outside"), (dict(which=-1), "which"), (dict(which=3), "which"),
+    (dict(limit=999), "limit"), (dict(limit=(1 << 31) + 1), "limit"), (dict(k=0), "n outside"), (dict(x=None), "NULL"),
+    (dict(w=P + 2), "aligned")])
+def test_linear_selftest_refusals(lib, kw, word):
+    a = dict(T=2, x=P, w=2 * P, which=0, limit=10_000)
+    cfg = B.LinearConfig(**{**LINEAR, **{k: v for k, v in kw.items() if k not in a}})
+    a.update({k: v for k, v in kw.items() if k in a})
+    refused(lib, lib.moe_w4a16_selftest_linear(ctypes.addressof(cfg), a["T"], a["x"], a["w"], 3 * P, a["which"],
+                                               a["limit"], None), word)

@@ -37,3 +37,28 @@ def test_selftest_argument_errors():
             assert ex.value.status == M.ERR_INVALID_ARG
     finally:
         m.close()
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("T,N,K", [(3, 256, 16384), (16, 130, 2048), (200, 300, 1024), (600, 512, 4096)])
+def test_linear_gives_up_and_the_context_survives(which, T, N, K):
+    """Warps of the matrix product stop early: the others' waits run out, the kernel ends, and the next call is right."""
+    import time
+
+    import torch
+    from w4a16_compact_expert_gb300 import block as B
+    g = torch.Generator().manual_seed(T)
+    x, w = torch.randn(T, K, generator=g).half().cuda(), (torch.randn(N, K, generator=g) / K ** 0.5).half().cuda()
+    ref = x.double() @ w.double().t()
+    assert B.status() == M.OK
+    t0 = time.monotonic()
+    B.selftest_timeout(x, w, which, 2_000_000)     # about a millisecond of SM cycles
+    torch.cuda.synchronize()
+    assert time.monotonic() - t0 < 20
+    assert B.status() == M.ERR_TIMEOUT
+    assert B.status() == M.OK                      # reported once, then cleared
+    out = B.linear(x, w)
+    # one rounding to FP16, FP32 sums over K / 16 steps
+    mag = x.double().abs() @ w.double().abs().t()
+    assert ((out.double() - ref).abs() <= 2.0 ** -11 * ref.abs() + (K / 16 + 16) * 2.0 ** -23 * 1.01 * mag + 2.0 ** -25).all()
+    assert B.status() == M.OK

@@ -57,6 +57,7 @@ def _lib():
     lib.moe_w4a16_route_scored.argtypes = [vp, i64] + [vp] * 5
     lib.moe_w4a16_linear.argtypes = [vp, i64] + [vp] * 8
     lib.moe_w4a16_block_status.argtypes = []
+    lib.moe_w4a16_selftest_linear.argtypes = [vp, i64, vp, vp, vp, ctypes.c_int32, i64, vp]
     return lib
 
 
@@ -153,6 +154,18 @@ def linear(x, w, *, bias=None, act: str = "none", residual=None, x_scale=None, w
 def status() -> int:
     """Synchronises and clears the status of the block operators: OK or ERR_TIMEOUT."""
     return _lib().moe_w4a16_block_status()
+
+
+def selftest_timeout(x, w, which: int, limit_cycles: int) -> None:
+    """Enqueue linear(x, w) with warps that stop early (see moe_w4a16_selftest_linear); x [T, K] and w [N, K] fp16."""
+    (T, K), N = x.shape, w.shape[0]
+    out = torch.empty(T, N, dtype=torch.float16, device=x.device)
+    cfg = LinearConfig(n=N, k=K)   # F16 in and out, no activation
+    lib = _lib()
+    st = lib.moe_w4a16_selftest_linear(ctypes.addressof(cfg), T, _m._ptr(x), _m._ptr(w), _m._ptr(out), int(which),
+                                       int(limit_cycles), _m._stream(None))
+    if st != _m.OK:
+        raise _m.MoEError(st, lib.moe_w4a16_last_error(None).decode())
 
 
 class MoEBlock:

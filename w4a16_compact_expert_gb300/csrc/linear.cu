@@ -39,7 +39,12 @@ struct LinearArgs {
   int act;
   uint32_t idesc;    // MMA instruction descriptor without its M and N fields
   int vec;           // 4: four neighbouring outputs can be read and written at once, else 1
+  // the self-test's: which warps stop early (GIVE_UP_*), and the limit of the others' waits
+  int give_up;
+  long long limit;
 };
+enum { GIVE_UP_MMA = 1, GIVE_UP_LOADS = 2, GIVE_UP_ODD_LOADS = 3 };
+constexpr int kGiveUpAt = 2;   // chunks before they stop
 
 // a / (1 + e^-a); the quotient is 0 where e^-a passes 2^126, as it should be.
 DEV_INLINE float silu(float a) { return a * blk::fast_rcp(1.f + blk::fast_exp(-a)); }
@@ -129,7 +134,7 @@ DEV_INLINE void umma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t
 }
 
 // Arrives on `bar` once the MMAs issued so far are done; the pair form at its
-// place in both CTAs.
+// place in the CTAs of the mask.
 DEV_INLINE void commit_one(uint64_t* bar, uint32_t leader) {
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
@@ -137,12 +142,12 @@ DEV_INLINE void commit_one(uint64_t* bar, uint32_t leader) {
       "r"(leader)
       : "memory");
 }
-DEV_INLINE void commit_pair(uint64_t* bar, uint32_t leader) {
+DEV_INLINE void commit_pair(uint64_t* bar, uint32_t mask, uint32_t leader) {
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
       " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3), "r"(leader)
+      "h"((uint16_t)mask), "r"(leader)
       : "memory");
 }
 
@@ -290,6 +295,31 @@ DEV_INLINE void activate_quads(const LinearArgs& a, W w, Bi b, float (&g)[Q * 4]
   }
 }
 
+// How a CTA ends.  The waits of the pipelines are bounded; whoever gives up
+// leaves its loop, and the others' waits run out in turn.  Either way nothing
+// may be on its way to a CTA's shared memory, and no MMA in flight, when it
+// ends (a pair: when both do, at their last cluster barrier):
+//   - the warp that multiplies waits for the MMAs it issued;
+//   - the warp that loads waits for the last release of every stage it filled
+//     (a stage is released once its MMAs have read it, so its copies have
+//     landed too).  Where the multiplying warp stopped first none comes; when
+//     this wait runs out, a second has passed since the last copy was issued.
+// These waits are over by the time the epilogue is, and keep their full limit
+// in the self-test.
+template <int STAGES>
+DEV_INLINE void wait_released(uint64_t* empty, int filled) {
+  for (int s = 0; s < STAGES && s < filled; ++s) {
+    const int last = (filled - 1 - s) / STAGES;   // the stage's last fill, counted from 0
+    if (!mbar_wait_bounded(&empty[s], (uint32_t)(last & 1), &g_block_status)) break;
+  }
+}
+
+// The pipelines' waits.
+template <bool TEST>
+DEV_INLINE bool wait_for(uint64_t* bar, uint32_t parity, const LinearArgs& a) {
+  return mbar_wait_limit(bar, parity, &g_block_status, TEST ? a.limit : MOE_WAIT_CYCLES);
+}
+
 struct Pipe {   // stage index and phase parity of a ring
   int i = 0;
   uint32_t ph = 0;
@@ -326,7 +356,7 @@ struct NarrowCfg {
 DEV_INLINE void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 DEV_INLINE void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-template <bool F8, bool GATED, int NT>
+template <bool F8, bool GATED, int NT, bool TEST>
 __global__ void __launch_bounds__(192, 2)
     linear_narrow_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ CUtensorMap tmW,
                          const __grid_constant__ CUtensorMap tmX, int out_dtype, int S, int prefetch) {
@@ -390,7 +420,8 @@ __global__ void __launch_bounds__(192, 2)
     const uint32_t leader = elect_lane(), ring = smem_u32(smem), bars = smem_u32(full);
     int issued = 0;
     for (; issued < mine; ++issued) {
-      if (!mbar_wait_bounded(&empty[p.i], p.ph ^ 1u, &g_block_status)) break;
+      if (TEST && issued == kGiveUpAt && (a.give_up == GIVE_UP_LOADS || (a.give_up == GIVE_UP_ODD_LOADS && (rank & 1)))) break;
+      if (!wait_for<TEST>(&empty[p.i], p.ph ^ 1u, a)) break;
       const int c0 = (rank + issued * S) * kElem;
       const uint32_t dst = ring + (uint32_t)(p.i * C::kStage), bar = bars + (uint32_t)(p.i * 8);
       expect_bytes(bar, (uint32_t)C::kStage, leader);
@@ -399,12 +430,7 @@ __global__ void __launch_bounds__(192, 2)
       fetch<1>(dst + C::kA, &tmX, c0, t0, bar, leader);
       p.next(C::kStages);
     }
-    if (issued < mine) {   // gave up: the copies in flight land before the CTA ends
-      for (int s = 0; s < C::kStages && s < issued; ++s) {
-        const int last = s + (issued - 1 - s) / C::kStages * C::kStages;
-        mbar_wait_bounded(&full[s], (uint32_t)((last / C::kStages) & 1), &g_block_status);
-      }
-    }
+    wait_released<C::kStages>(empty, issued);
     __syncwarp();
   } else if (warp == 1) {
     Pipe p;
@@ -413,7 +439,8 @@ __global__ void __launch_bounds__(192, 2)
     const uint32_t d = __reduce_or_sync(0xffffffffu, tmem);   // the same in every lane, and known to be
     const uint64_t desc0 = sw128_desc(smem_u32(smem));        // its address field counts 16 bytes
     for (int k = 0; k < mine; ++k) {
-      if (!mbar_wait_bounded(&full[p.i], p.ph, &g_block_status)) break;
+      if (TEST && k == kGiveUpAt && a.give_up == GIVE_UP_MMA) break;
+      if (!wait_for<TEST>(&full[p.i], p.ph, a)) break;
       tc_fence_after();
       const uint64_t ad = desc0 + (uint64_t)(p.i * (C::kStage / 16)), bd = ad + C::kA / 16;
 #pragma unroll
@@ -423,10 +450,10 @@ __global__ void __launch_bounds__(192, 2)
       p.next(C::kStages);
     }
     commit_one(done, leader);
+    mbar_wait_bounded(done, 0, &g_block_status);
     __syncwarp();
   } else {
-    ok = mbar_wait_bounded(done, 0, &g_block_status);   // every stage has been consumed
-    __syncwarp();
+    ok = __all_sync(0xffffffffu, wait_for<TEST>(done, 0, a));   // every stage has been consumed
   }
 
   // Token c of the tile belongs to rank c % S: every CTA sends its part of c's
@@ -548,7 +575,7 @@ struct WideCfg {
   static constexpr int kStages = 192 * 1024 / kStage;
   static constexpr int kEpiWarps = 8, kParts = kEpiWarps / 4;   // kParts warps per TMEM lane quarter
   static constexpr int kTurn = 32 * 32 * 4;   // per epilogue warp: 32 rows x 32 FP32 columns
-  static constexpr int kBars = 2 * kStages + 4;
+  static constexpr int kBars = 2 * kStages + 5;
   static constexpr int kSmem = kStages * kStage + kEpiWarps * kTurn + kBars * 8 + 16 + 1024;
   static constexpr int kThreads = (2 + kEpiWarps) * 32;   // warp 0 loads, warp 1 multiplies, the others finish
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -615,7 +642,7 @@ DEV_INLINE void finish_turned(const LinearArgs& a, const float* buf, int t0, int
   store_quads<O, kPass>(a, t, live, n0 + c, step, v);
 }
 
-template <bool F8, bool GATED, int BN, typename O>
+template <bool F8, bool GATED, int BN, typename O, bool TEST>
 __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     linear_wide_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmX) {
@@ -630,7 +657,8 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;   // [2]
   uint64_t* acc_empty = acc_full + 2;        // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* last = acc_empty + 2;            // every MMA of the pair is done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(last + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int mtiles = (a.T + 255) / 256, tiles = mtiles * ((a.N + FT - 1) / FT);
@@ -650,6 +678,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
       mbar_init(&acc_full[s], 1);
       mbar_init(&acc_empty[s], 2 * C::kEpiWarps);
     }
+    mbar_init(last, 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -675,7 +704,8 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
       const int m0 = (tile % mtiles) * 256 + rank * 128, n0 = tile / mtiles * FT;
       const int b0 = rank == 0 ? n0 : GATED ? a.N + n0 : n0 + BN / 2;   // this CTA's weight rows
       for (int k = 0; k < nk; ++k) {
-        if (!mbar_wait_bounded(&empty[p.i], p.ph ^ 1u, &g_block_status)) {
+        if ((TEST && issued == kGiveUpAt && (a.give_up == GIVE_UP_LOADS || (a.give_up == GIVE_UP_ODD_LOADS && rank))) ||
+            !wait_for<TEST>(&empty[p.i], p.ph ^ 1u, a)) {
           ok = false;
           break;
         }
@@ -687,12 +717,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
         p.next(C::kStages);
       }
     }
-    if (!ok && rank == 0) {   // gave up: the copies in flight land before the CTAs end
-      for (int s = 0; s < C::kStages && s < issued; ++s) {
-        const int last = s + (issued - 1 - s) / C::kStages * C::kStages;
-        mbar_wait_bounded(&full[s], (uint32_t)((last / C::kStages) & 1), &g_block_status);
-      }
-    }
+    wait_released<C::kStages>(empty, issued);
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
@@ -703,11 +728,11 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
       const uint32_t tm = __reduce_or_sync(0xffffffffu, tmem);
       const uint64_t desc0 = sw128_desc(smem_u32(smem));
       for (int tile = first; tile < tiles && ok; tile += step) {
-        if (!mbar_wait_bounded(&acc_empty[acc.i], acc.ph ^ 1u, &g_block_status)) break;
+        if (!wait_for<TEST>(&acc_empty[acc.i], acc.ph ^ 1u, a)) break;
         tc_fence_after();
         const uint32_t d = tm + (uint32_t)(acc.i * BN);
         for (int k = 0; k < nk; ++k) {
-          if (!mbar_wait_bounded(&full[p.i], p.ph, &g_block_status)) {
+          if ((TEST && k == kGiveUpAt && a.give_up == GIVE_UP_MMA) || !wait_for<TEST>(&full[p.i], p.ph, a)) {
             ok = false;
             break;
           }
@@ -716,12 +741,14 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             umma<F8, 2>(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (uint32_t)((k | j) != 0), leader);
-          commit_pair(&empty[p.i], leader);
+          commit_pair(&empty[p.i], 3, leader);
           p.next(C::kStages);
         }
-        if (ok) commit_pair(&acc_full[acc.i], leader);
+        if (ok) commit_pair(&acc_full[acc.i], 3, leader);
         acc.next(2);
       }
+      commit_pair(last, 1, leader);
+      mbar_wait_bounded(last, 0, &g_block_status);
     }
     __syncwarp();
   } else {
@@ -758,7 +785,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
         if (a.bias) cb = load_columns(a, a.bias + up, n, apart);
       }
       __syncwarp();
-      if (!mbar_wait_bounded(&acc_full[acc.i], acc.ph, &g_block_status)) break;
+      if (!__all_sync(0xffffffffu, wait_for<TEST>(&acc_full[acc.i], acc.ph, a))) break;
       tc_fence_after();
       const uint32_t d = tmem + (uint32_t)(acc.i * BN) + ((uint32_t)(q * 32) << 16);
       for (int c0 = h * kPart; c0 < (h + 1) * kPart; c0 += kStep) {   // kStep output features at a time
@@ -801,7 +828,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();   // nothing of the peer is still on its way here
+  cluster_sync();   // nothing is on its way to either CTA (see wait_released)
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
@@ -898,7 +925,7 @@ int split_of(int tiles, int nk, const int (&alone)[9], const int (&shared)[9]) {
   return best;
 }
 
-template <bool F8, bool GATED, int NT>
+template <bool F8, bool GATED, int NT, bool TEST = false>
 cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
   using C = NarrowCfg<NT>;
   constexpr int FT = GATED ? 64 : 128;
@@ -906,7 +933,7 @@ cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
   if (!encode_rows(&mw, p.w, GATED ? 2ll * p.a.N : p.a.N, p.a.K, p.elem, p.ld_w, FT) ||
       !encode_rows(&mx, p.x, p.a.T, p.a.K, p.elem, p.ld_x, NT))
     return cudaErrorInvalidValue;
-  auto kernel = linear_narrow_kernel<F8, GATED, NT>;
+  auto kernel = linear_narrow_kernel<F8, GATED, NT, TEST>;
   const cudaError_t e = opt_in_smem((const void*)kernel, C::kSmem);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)((p.a.N + FT - 1) / FT) * ((p.a.T + NT - 1) / NT);
@@ -934,14 +961,14 @@ cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
                     prefetch);
 }
 
-template <bool F8, bool GATED, int BN, typename O>
+template <bool F8, bool GATED, int BN, typename O, bool TEST = false>
 cudaError_t launch_wide_o(const Problem& p, cudaStream_t st) {
   using C = WideCfg<BN>;
   CUtensorMap mw, mx;
   if (!encode_rows(&mw, p.w, GATED ? 2ll * p.a.N : p.a.N, p.a.K, p.elem, p.ld_w, BN / 2) ||
       !encode_rows(&mx, p.x, p.a.T, p.a.K, p.elem, p.ld_x, 128))
     return cudaErrorInvalidValue;
-  auto kernel = linear_wide_kernel<F8, GATED, BN, O>;
+  auto kernel = linear_wide_kernel<F8, GATED, BN, O, TEST>;
   cudaError_t e = opt_in_smem((const void*)kernel, C::kSmem);
   if (e != cudaSuccess) return e;
   static std::atomic<int> resident[kMaxDevices];   // clusters that run at once, asked once per device
@@ -1010,14 +1037,10 @@ cudaError_t launch_linear(const Problem& p, cudaStream_t st) {
 
 int elem_size(int dtype) { return dtype == MOE_W4A16_E4M3 ? 1 : dtype == MOE_W4A16_F32 ? 4 : 2; }
 
-}  // namespace
-
-extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linear_config* cfg, int64_t T,
-                                                           const void* x, const void* w, const float* x_scale,
-                                                           const float* w_scale, const float* bias,
-                                                           const void* residual, void* out,
-                                                           moe_w4a16_stream_t stream) try {
-  const char* op = "linear";
+// give_up nonzero: the self-test, with the limit of its waits.
+moe_w4a16_status run_linear(const char* op, const moe_w4a16_linear_config* cfg, int64_t T, const void* x, const void* w,
+                            const float* x_scale, const float* w_scale, const float* bias, const void* residual,
+                            void* out, moe_w4a16_stream_t stream, int give_up, int64_t limit) {
   if (!cfg) return blk::reject(op, "cfg is NULL");
   const moe_w4a16_linear_config c = *cfg;
   const bool f8 = c.in_dtype == MOE_W4A16_E4M3;
@@ -1075,9 +1098,40 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linea
   const size_t vb = 4 * (size_t)os;
   p.a.vec = blk::aligned(out, vb) && ld_out % 4 == 0 && (!residual || (blk::aligned(residual, vb) && ld_res % 4 == 0)) ? 4 : 1;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = f8 ? launch_linear<true>(p, st) : launch_linear<false>(p, st);
+  p.a.give_up = give_up;
+  p.a.limit = limit;
+  const cudaError_t e = give_up ? (T <= 16 ? launch_narrow<false, false, 16, true>(p, st)
+                                           : launch_wide_o<false, false, 128, __half, true>(p, st))
+                        : f8    ? launch_linear<true>(p, st)
+                                : launch_linear<false>(p, st);
   return e == cudaSuccess ? MOE_W4A16_OK : blk::launch_failed(op, e);
+}
+
+}  // namespace
+
+extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linear_config* cfg, int64_t T,
+                                                           const void* x, const void* w, const float* x_scale,
+                                                           const float* w_scale, const float* bias,
+                                                           const void* residual, void* out,
+                                                           moe_w4a16_stream_t stream) try {
+  return run_linear("linear", cfg, T, x, w, x_scale, w_scale, bias, residual, out, stream, 0, 0);
 } catch (...) {   // the host's heap is full
+  return MOE_W4A16_ERR_OOM;
+}
+
+extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_selftest_linear(const moe_w4a16_linear_config* cfg, int64_t T,
+                                                                    const void* x, const void* w, void* out,
+                                                                    int32_t which, int64_t limit_cycles,
+                                                                    moe_w4a16_stream_t stream) try {
+  const char* op = "selftest_linear";
+  if (!cfg) return blk::reject(op, "cfg is NULL");
+  if (cfg->in_dtype != MOE_W4A16_F16 || cfg->out_dtype != MOE_W4A16_F16 || cfg->act != MOE_W4A16_ACT_NONE)
+    return blk::reject(op, "takes F16 in and out and no activation");
+  if (T < 1 || (T > 16 && T <= 64)) return blk::reject(op, "T outside [1, 16] and (64, 2^30]");
+  if (which < 0 || which > 2) return blk::reject(op, "which outside [0, 2]");
+  if (limit_cycles < 1000 || limit_cycles > MOE_WAIT_CYCLES) return blk::reject(op, "limit_cycles outside [1000, 2^31]");
+  return run_linear(op, cfg, T, x, w, nullptr, nullptr, nullptr, nullptr, out, stream, GIVE_UP_MMA + which, limit_cycles);
+} catch (...) {
   return MOE_W4A16_ERR_OOM;
 }
 

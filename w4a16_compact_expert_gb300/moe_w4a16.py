@@ -28,7 +28,8 @@ EXPORTED = ["moe_w4a16_create", "moe_w4a16_destroy", "moe_w4a16_pack_experts", "
             "moe_w4a16_cache_release", "moe_w4a16_cache_get_stats", "moe_w4a16_cache_slot_of",
             "moe_w4a16_cache_last_error", "moe_w4a16_cache_create_sim", "moe_w4a16_cache_sim_complete",
             "moe_w4a16_cache_sim_fail", "moe_w4a16_selftest_timeout", "moe_w4a16_offload_enable", "moe_w4a16_add_rmsnorm",
-            "moe_w4a16_route_scored", "moe_w4a16_linear", "moe_w4a16_block_status", "moe_w4a16_forward_routed"]
+            "moe_w4a16_route_scored", "moe_w4a16_linear", "moe_w4a16_block_status", "moe_w4a16_forward_routed",
+            "moe_w4a16_selftest_linear"]
 PATH_NONE, PATH_DECODE_FUSED, PATH_DECODE, PATH_GEMM, PATH_OFFLOAD = 0, 1, 2, 3, 4
 PATH_NAMES = {PATH_NONE: "none", PATH_DECODE_FUSED: "decode_fused", PATH_DECODE: "decode", PATH_GEMM: "gemm",
               PATH_OFFLOAD: "offload_qpacked"}

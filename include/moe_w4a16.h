@@ -561,7 +561,11 @@ typedef struct {
  * (N, K and T may be odd; the stride of a single row is not used).  Products accumulate in FP32 on the tensor cores;
  * with few tokens K is split over the CTAs of a cluster and the parts are
  * added in a fixed order, so a call's result does not change from run to
- * run.  A bounded device wait that gave up is reported by
+ * run.  The activations use one-instruction exponentials and reciprocals; the
+ * relative error of act(a), in units of 2^-24, is at most 2 |a| + 8 (SILU and
+ * the silu of SWIGLU), 9 E + 8 with E = 2 sqrt(2/pi) (|a| + 0.044715 |a|^3)
+ * (GELU_TANH) and 110 + 1.5 a^2 (GELU), which shows in F32 outputs only; values
+ * smaller than about 2^-119 may come out as 0.  A bounded device wait that gave up is reported by
  * moe_w4a16_block_status. */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linear_config* cfg, int64_t T, const void* x,
                                                 const void* w, const float* x_scale, const float* w_scale,

@@ -46,7 +46,8 @@ struct LinearArgs {
 enum { GIVE_UP_MMA = 1, GIVE_UP_LOADS = 2, GIVE_UP_ODD_LOADS = 3 };
 constexpr int kGiveUpAt = 2;   // chunks before they stop
 
-// a / (1 + e^-a); the quotient is 0 where e^-a passes 2^126, as it should be.
+// a / (1 + e^-a), relative error up to (2 |a| + 8) 2^-24; 0 where e^-a passes
+// 2^126 and the result is smaller than 87 2^-126.
 DEV_INLINE float silu(float a) { return a * blk::fast_rcp(1.f + blk::fast_exp(-a)); }
 
 // a Phi(a) of two values with the normal distribution's tail Phi(-|a|) =
@@ -55,7 +56,9 @@ DEV_INLINE float silu(float a) { return a * blk::fast_rcp(1.f + blk::fast_exp(-a
 // coefficients fitted in 64 bits (reweighted least squares over 0 <= |a| <= 14)
 // to a relative error of 1.4e-7 near 0 that may grow to 4.2e-6 far out; the
 // book's five terms are as near at 0 and 2 % off at a = -9.  Taken from the
-// tail's side, so that large negative a keep their relative accuracy.
+// tail's side, so that large negative a keep their relative accuracy: as
+// evaluated here 6.3e-6 down to a = -8 and 9.4e-6 at -12, where the rounding of
+// a^2 / 2 shows; the result is 0 below a = -13.
 DEV_INLINE float2 gelu(float2 a) {
   auto both = [](float c) { return make_float2(c, c); };
   const float2 d = blk::fma2(both(0.35f), make_float2(fabsf(a.x), fabsf(a.y)), both(1.f));
@@ -72,7 +75,8 @@ DEV_INLINE float2 gelu(float2 a) {
   return blk::mul2(a, make_float2(a.x > 0.f ? head.x : tail.x, a.y > 0.f ? head.y : tail.y));
 }
 
-// (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+// (1 + tanh u) / 2 = 1 / (1 + e^-2u); relative error up to (18 |u| + 8) 2^-24, 0
+// where e^-2u passes 2^126.
 DEV_INLINE float gelu_tanh(float a) {
   const float u = 0.7978845608f * fmaf(0.044715f * a, a * a, a);
   return a * blk::fast_rcp(1.f + blk::fast_exp(-2.f * u));

@@ -173,3 +173,39 @@ def test_linear_selftest_refusals(lib, kw, word):
     a.update({k: v for k, v in kw.items() if k in a})
     refused(lib, lib.moe_w4a16_selftest_linear(ctypes.addressof(cfg), a["T"], a["x"], a["w"], 3 * P, a["which"],
                                                a["limit"], None), word)
+
+
+def test_routed_forward_takes_the_stream_of_the_layers_device(monkeypatch):
+    class OnDevice:   # what forward_routed looks at of a CUDA tensor
+        def __init__(self, t):
+            self.dtype, self.shape, self.device, self.dim = t.dtype, t.shape, "cuda:1", t.dim
+
+        def get_device(self):
+            return 1
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return P
+
+    class Stream:
+        def __init__(self, device):
+            self.cuda_stream = 1000 + (0 if device is None else device)
+
+    calls = []
+
+    class Lib:
+        def moe_w4a16_forward_routed(self, *a):
+            calls.append(a)
+            return F.OK
+
+        def moe_w4a16_destroy(self, h):
+            pass
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(device))
+    m = object.__new__(F.MoELayer)
+    m.h, m.lib, m.cfg = None, Lib(), F.Config(hidden=64, inter=64, num_experts=4, top_k=2, device=1)
+    x = OnDevice(torch.zeros(3, 64, dtype=torch.float16))
+    m.forward_routed(x, OnDevice(torch.zeros(3, 2, dtype=torch.int32)), OnDevice(torch.zeros(3, 2)), out=x)
+    assert calls[0][-1] == 1001

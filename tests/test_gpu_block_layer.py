@@ -219,3 +219,19 @@ def test_routed_weight_zero_contributes_exactly_nothing(force):
         gp.assert_output(out.float().cpu().numpy().astype(np.float64), oracle_routed(layer, x, ids, w), np.ones(6, bool))
     finally:
         m.close()
+
+
+def test_routed_output_is_allocated_for_the_stream(tiny, monkeypatch):
+    import torch
+    layer, m = tiny
+    x, ids, w = gp.to_dev(synth.draw_x(5, 4, 256)), torch.zeros(4, 2, dtype=torch.int32, device="cuda"), torch.ones(4, 2).cuda()
+    torch.cuda.synchronize()
+    side, seen = torch.cuda.Stream(), []
+    empty_like = torch.empty_like
+    monkeypatch.setattr(torch, "empty_like", lambda t: (seen.append(torch.cuda.current_stream()), empty_like(t))[1])
+    out = m.forward_routed(x, ids, w, stream=side)
+    side.synchronize()
+    assert seen == [side]
+    assert torch.equal(out, m.forward_routed(x, ids, w))
+    torch.cuda.synchronize()
+    assert seen == [side, torch.cuda.current_stream()]

@@ -128,10 +128,11 @@ def _ptr(a) -> Optional[int]:
     return a.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device: Optional[int] = None) -> Optional[int]:
+    """The stream's handle; None: the current stream of the device (default: of the current device)."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        stream = torch.cuda.current_stream(device)
     return stream.cuda_stream
 
 
@@ -225,7 +226,8 @@ class MoELayer:
     def forward_routed(self, x, ids, weights, flags: int = 0, out=None, stream=None):
         """The experts on given routing: x cuda fp16 [T, H], ids int32 and weights fp32 [T, top_k], on the layer's device.
 
-        An id may occur more than once in a row; one outside [0, E) contributes nothing and counts as a miss."""
+        An id may occur more than once in a row; one outside [0, E) contributes nothing and counts as a miss.  With
+        stream=None work goes to the current stream of the layer's device; out is allocated for the stream."""
         import torch
         T = int(x.shape[0])
         if ids.dtype != torch.int32 or weights.dtype != torch.float32 or ids.shape != (T, self.cfg.top_k) or \
@@ -236,11 +238,12 @@ class MoELayer:
         if any(t.get_device() != self.cfg.device for t in (x, ids, weights)):
             raise ValueError("x, ids and weights must be on the layer's CUDA device")
         if out is None:
-            out = torch.empty_like(x)
+            with torch.cuda.stream(stream):   # None: as it is
+                out = torch.empty_like(x)
         elif out.dtype != x.dtype or out.shape != x.shape or out.device != x.device:
             raise ValueError("out must have x's type, shape and device")
         self._check(self.lib.moe_w4a16_forward_routed(self.h, _ptr(x), T, _ptr(ids), _ptr(weights), flags, _ptr(out),
-                                                      _stream(stream)))
+                                                      _stream(stream, self.cfg.device)))
         return out
 
     def forward_raw(self, x_ptr: int, T: int, router_w_ptr: int, bias_ptr, flags: int, out_ptr: int, stream_ptr):

@@ -209,3 +209,10 @@ def test_routed_forward_takes_the_stream_of_the_layers_device(monkeypatch):
     x = OnDevice(torch.zeros(3, 64, dtype=torch.float16))
     m.forward_routed(x, OnDevice(torch.zeros(3, 2, dtype=torch.int32)), OnDevice(torch.zeros(3, 2)), out=x)
     assert calls[0][-1] == 1001
+
+
+def test_another_torch_rebuilds_the_binding(monkeypatch):
+    build_ext.build()
+    assert build_ext.up_to_date()
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert not build_ext.up_to_date()

@@ -21,6 +21,7 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libmoe_w4a16.so")
 BINDING_SRC = os.path.join(CSRC, "block_binding.cpp")
 BINDING = os.path.join(OUT_DIR, "_block.so")
+STAMP = os.path.join(OUT_DIR, "_block.txt")   # what the binding was built against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -46,8 +47,24 @@ def _newer(target, deps) -> bool:
     return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
 
 
+def _built_against() -> str:
+    """The versions that the binding's ABI depends on."""
+    import sys
+
+    import torch
+    return f"torch {torch.__version__}, CXX11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, python {sys.version.split()[0]}"
+
+
+def _stamped() -> bool:
+    try:
+        with open(STAMP) as f:
+            return f.read() == _built_against()
+    except OSError:
+        return False
+
+
 def up_to_date() -> bool:
-    return _newer(LIB, _deps()) and _newer(BINDING, [BINDING_SRC, LIB, __file__])
+    return _newer(LIB, _deps()) and _newer(BINDING, [BINDING_SRC, LIB, __file__]) and _stamped()
 
 
 def _compile_binding() -> str:
@@ -78,6 +95,8 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(BINDING + ".tmp", BINDING)
+    with open(STAMP, "w") as f:
+        f.write(_built_against())
     os.remove(obj)
 
 

@@ -374,11 +374,7 @@ __global__ void __launch_bounds__(192, 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int FT = GATED ? 64 : 128;   // output features per tile
-  // the CTAs of a cluster are neighbours in x; then the token tiles of one
-  // weight tile, so that W comes from L2 after its first reader
-  const int rank = blockIdx.x % S, tile = blockIdx.x / S;
-  const int ntt = (a.T + NT - 1) / NT;
-  const int t0 = (tile % ntt) * NT, n0 = (tile / ntt) * FT;
+  const int rank = blockIdx.x % S, n0 = blockIdx.x / S * FT;   // T <= NT: a tile holds all tokens
   const int nk = (a.K + kElem - 1) / kElem;
   // rank r takes the chunks r, r + S, ..: the cluster reads neighbouring
   // 128-byte pieces of a weight row at about the same time
@@ -431,7 +427,7 @@ __global__ void __launch_bounds__(192, 2)
       expect_bytes(bar, (uint32_t)C::kStage, leader);
       fetch<1>(dst, &tmW, c0, n0, bar, leader);
       if (GATED) fetch<1>(dst + FT * kChunk, &tmW, c0, a.N + n0, bar, leader);
-      fetch<1>(dst + C::kA, &tmX, c0, t0, bar, leader);
+      fetch<1>(dst + C::kA, &tmX, c0, 0, bar, leader);
       p.next(C::kStages);
     }
     wait_released<C::kStages>(empty, issued);
@@ -468,7 +464,7 @@ __global__ void __launch_bounds__(192, 2)
   } else if (!C::kOwnRecv) {
     __syncthreads();
   }
-  const int nt = min(NT, a.T - t0), cap = (NT + S - 1) / S;
+  const int nt = min(NT, a.T), cap = (NT + S - 1) / S;
   const uint32_t recv = smem_u32(smem + C::kRecvAt);
   if (warp >= 2) {
     const int q = warp & 3, row = q * 32 + lane;
@@ -528,7 +524,7 @@ __global__ void __launch_bounds__(192, 2)
       for (int q = 0; q < kBatch; ++q) {
         const int sl = s + q * kSweep;
         live[q] = sl < own;
-        t[q] = t0 + min(sl, own - 1) * S + rank;
+        t[q] = min(sl, own - 1) * S + rank;
         const float* p = parts + min(sl, own - 1) * 128;
         if (wide) {
 #pragma unroll 4
@@ -940,7 +936,7 @@ cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
   auto kernel = linear_narrow_kernel<F8, GATED, NT, TEST>;
   const cudaError_t e = opt_in_smem((const void*)kernel, C::kSmem);
   if (e != cudaSuccess) return e;
-  const long long tiles = (long long)((p.a.N + FT - 1) / FT) * ((p.a.T + NT - 1) / NT);
+  const int tiles = (p.a.N + FT - 1) / FT;
   const int nk = (p.a.K + kChunk / p.elem - 1) / (kChunk / p.elem);
   // asked once per device; racing first calls ask twice and store the same
   static std::atomic<int> known[kMaxDevices][2][9];
@@ -955,8 +951,7 @@ cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
         known[p.dev][two][s].store(n, std::memory_order_relaxed);
       }
     }
-  const int S = tiles > (1 << 24) ? 1 : split_of((int)tiles, nk, fit[0], fit[1]);
-  if (tiles * S > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const int S = split_of(tiles, nk, fit[0], fit[1]);
   // Grids of more CTAs than SMs keep the memory busy to their end, and the next
   // grid's prefetch takes over there (W [11264][2048] FP16 9.8 -> 9.3 us);
   // smaller ones it holds up (W [2048][5632] 8.9 -> 9.6, [64][2048] 3.2 -> 4.1).

@@ -84,3 +84,20 @@ def test_saturated_scores_by_hand():
     logits = torch.tensor([[40.0, 50.0, 1.0, 2.0], [50.0, 2.0, 40.0, 45.0]], device="cuda")
     assert check_route(logits, None, 2, score="sigmoid")[0].tolist() == [[0, 1], [0, 2]]
     assert check_route(logits, None, 1, score="sigmoid", groups=2, top_groups=1)[0].tolist() == [[0], [0]]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(64, 8), (84, 2), (20, 5), (32, 16), (60, 20), (512, 32)])
+def test_infinite_biases_in_groups(score, E, groups):
+    """A group with one infinite choice is as good as one with two, or with more."""
+    logits = rand((24, E), torch.float32, E)
+    g = torch.Generator().manual_seed(E)
+    for p in (0.05, 0.3, 0.8):
+        bias = torch.randn(E, generator=g)
+        bias[torch.rand(E, generator=g) < p] = INF
+        bias[torch.rand(E, generator=g) < 0.2] = -INF
+        bias[torch.rand(E, generator=g) < 0.1] = 3.4e38
+        for top in (1, groups // 2, groups - 1):
+            for rank in (1, 2):
+                check_route(logits, bias.cuda(), min(6, top * (E // groups)), score=score, groups=groups,
+                            top_groups=max(top, 1), group_rank=rank)

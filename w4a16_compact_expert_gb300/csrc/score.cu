@@ -350,7 +350,7 @@ DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
       b1 = max(b1, o1);
     }
     // What ranks the groups: logits, or half their value (so that no sum
-    // overflows; an infinite bias counts as the largest number) with a bound of
+    // overflows; an infinite one counts as twice the largest number) with a bound of
     // its FP32 error: half of `slack` for each choice's score, and the roundings
     // of the choices and of their sum, a unit each and taken twice, which count
     // by the choices' own size: of opposite sign they may cancel.
@@ -363,6 +363,7 @@ DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
         gv = score_of(a, gv, m, den);
         if (v2 != -INFINITY) v2 = score_of(a, v2, m, den);
       }
+      if (a.two && gv == INFINITY) v2 = gv;   // infinite, whatever the other
       gv = fminf(gv, largest);
       err = 0.25f * slack + 2.f * unit * fminf(fabsf(gv), largest);
       gv *= 0.5f;

@@ -518,7 +518,9 @@ typedef struct {
  *           values stay eligible (ties: lower group)
  *   topk_ids [t][k] = the k largest choices, largest first (ties: lower
  *           expert index);  topk_w = score[topk_ids] (/ their sum) * scale
- * The bias decides the selection only; the weights come from the scores.
+ * The bias decides the selection only; the weights come from the scores
+ * (renormalised softmax weights from the chosen logits, so that none
+ * underflows beside a larger logit that was not chosen).
  * The ids are those that 64-bit arithmetic gives: where two choices (or two
  * groups) lie closer than the error of the FP32 scores, they are redone in
  * FP64.  Different logits whose 64-bit scores are equal (sigmoids of 38 and 50

@@ -4,7 +4,8 @@ their logits differ."""
 import pytest
 import torch
 
-from tests.test_gpu_block import check_route, rand
+from tests.test_gpu_block import N32, check_route, rand
+from w4a16_compact_expert_gb300 import block as B
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -101,3 +102,18 @@ def test_infinite_biases_in_groups(score, E, groups):
             for rank in (1, 2):
                 check_route(logits, bias.cuda(), min(6, top * (E // groups)), score=score, groups=groups,
                             top_groups=max(top, 1), group_rank=rank)
+
+
+@pytest.mark.parametrize("E,groups,top", [(16, 1, 1), (64, 8, 2), (60, 5, 2), (300, 1, 1)])
+@pytest.mark.parametrize("m", [INF, 900.0, 60.0])
+def test_renormalised_softmax_weights_do_not_underflow(E, groups, top, m):
+    """A bias selects experts whose softmax is 0 in 64 bits beside the largest logit; the weights are relative to the
+    largest chosen, whichever way the token's order was decided."""
+    logits = rand((64, E), torch.float32, E)
+    logits[:, E - 1] = m
+    bias = torch.zeros(E, device="cuda")
+    bias[E - 1] = -2000.0
+    ids, w = B.route_scored(logits, 3, bias=bias, groups=groups, top_groups=top, renormalize=True, scale=2.0)
+    assert m == 60.0 or (ids == torch.arange(3, device="cuda")).all()
+    ref = 2.0 * torch.softmax(logits.double().gather(1, ids.long()), -1)
+    assert ((w.double() - ref).abs() <= N32 * ref).all()

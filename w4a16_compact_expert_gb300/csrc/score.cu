@@ -118,8 +118,7 @@ __device__ __noinline__ void choose_exact(const ScoreArgs& a, long long t, unsig
   float mf = -INFINITY;
 #pragma unroll 1
   for (int e = lane; e < a.E; e += 32) mf = fmaxf(mf, logit_at<E>(a, t, e));
-  const double m = warp_max_f(mf);
-  double den = 0;
+  double m = warp_max_f(mf), den = 0;
   if (!a.sigmoid) {
 #pragma unroll 1
     for (int e = lane; e < a.E; e += 32) {
@@ -191,8 +190,13 @@ __device__ __noinline__ void choose_exact(const ScoreArgs& a, long long t, unsig
     __syncwarp();
   }
   const bool chosen = lane < a.k && mine > kNone64;
-  const double s = chosen ? score((double)logit_at<E>(a, t, my_e)) : 0.0;
+  const float my_l = chosen ? logit_at<E>(a, t, my_e) : -INFINITY;
   double sum = 1.0;
+  if (a.renorm && !a.sigmoid) {   // the denominator cancels; relative to the largest chosen, so that none is lost
+    m = warp_max_f(my_l);
+    den = 1.0;
+  }
+  const double s = score((double)my_l);
   if (a.renorm) {
     sum = s;
 #pragma unroll 1

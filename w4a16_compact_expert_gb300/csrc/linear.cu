@@ -11,14 +11,14 @@
 // of a token's row to that token's owner in the cluster, which adds the parts
 // in rank order and finishes the row (no workspace, no atomics, one launch).
 // For SWIGLU the 128 rows are 64 gate rows and the matching 64 up rows.
-// W [11264][2048] FP16, one token: 9.3 us, 5.0 TB/s; W [8192][28672] 6.8 TB/s.
+// W [11264][2048] FP16, one token: 9.5 us, 4.8 TB/s; W [8192][28672] 6.8 TB/s.
 //
 // linear_wide_kernel (more tokens; bound by the tensor cores, or by the few
 // tiles of a short problem): persistent CTA pairs (cta_group::2) over tiles
 // of 256 tokens x 256, 128 or 64 weight rows, two accumulators, so that one
 // tile's epilogue runs under the next tile's MMAs.
-// T = 2048, W [11264][2048]: E4M3 33 us (2,840 TFLOP/s), FP16 55 us (1,710); T =
-// 4096, W [11264][5632] E4M3 140 us (3,700).
+// T = 2048, W [11264][2048]: E4M3 37.4 us (2,530 TFLOP/s; 34 in a loop of this
+// call alone), FP16 56 us (1,690); T = 4096, W [2048][5632] FP16 69 us (1,370).
 #include <cuda.h>
 #include <type_traits>
 
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
       // the lanes below 16, of the up rows above).  T = 2048, N = 2048, K = 1024
       // FP16 with residual 14.4 -> 13.1 us, with bias 11.8 -> 11.5; T = 2048, N =
       // 4096, K = 2048 E4M3 18.8 -> 17.0; SWIGLU N = 5632 E4M3 35.5 -> 33.1, with
-      // bias 40.6 -> 35.0.
+      // bias 40.6 -> 35.0 (loops of one call; E4M3 SWIGLU among others 37.8 -> 37.6).
       if (a.res && t0 + lane < a.T) {
         const int n = n0 + h * kPart, left = min(kPart, a.N - n);
         const O* p = static_cast<const O*>(a.res) + (size_t)(t0 + lane) * a.ld_res + n;

@@ -557,7 +557,8 @@ DEV_INLINE bool choose(const ScoreArgs& a, long long t, uint32_t* cell) {
 }
 
 // CTAs per SM (registers) as measured best at T = 16384: 256 experts in groups
-// with a bias 18.1 us with 4, 20.8 with 6; 64 experts 7.5 with 6, 8.5 with 4.
+// with a bias 18.1 us with 4, 20.8 with 6; 64 experts 7.5 with 6, 8.5 with 4
+// (19.3 and 8.0 since groups carry their own bounds and ties are looked for).
 template <int EPL>
 constexpr int kCtas = EPL <= 2 ? 6 : EPL == 4 ? 5 : EPL == 8 ? 4 : 3;
 

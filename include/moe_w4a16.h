@@ -456,6 +456,11 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_sim_fail(moe_w4a16_cache* c, int3
  *   moe_w4a16_route_scored  expert ids and weights from router logits:
  *                           softmax or sigmoid scores, a balancing bias,
  *                           groups, top-k, renormalised weights
+ *   moe_w4a16_add_rmsnorm_blocks  the norm with its 8-bit copy in blocks: a
+ *                           scale per row and 128 values
+ *   moe_w4a16_token_logprobs  log probabilities of given tokens, entropies and
+ *                           the most likely tokens, from the logits of an
+ *                           output head
  *
  * They need no handle, allocate nothing and keep nothing between calls.
  * Work is enqueued on `stream` (the calling thread's current device); calls
@@ -493,6 +498,17 @@ typedef struct {
 MOE_W4A16_API moe_w4a16_status moe_w4a16_add_rmsnorm(const moe_w4a16_rmsnorm_config* cfg, int64_t T, const void* x,
                                                      const void* residual, const void* weight, void* residual_out,
                                                      void* y, void* q, float* q_scale, moe_w4a16_stream_t stream);
+
+/* moe_w4a16_add_rmsnorm with an E4M3 copy that has a scale per row and 128 values
+ * (the last block of a row may be shorter): with nb = ceil(H / 128)
+ *   q_scale[t][j] = max over block j of |n| / 448     ([T][nb], contiguous)
+ *   q[t][h] = n / q_scale[t][h / 128] in E4M3, saturating
+ * Both are required; y and residual_out as there.  A block whose q_scale would
+ * fall below 2^-126 gets q_scale = 0 and q = 0. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_add_rmsnorm_blocks(const moe_w4a16_rmsnorm_config* cfg, int64_t T,
+                                                            const void* x, const void* residual, const void* weight,
+                                                            void* residual_out, void* y, void* q, float* q_scale,
+                                                            moe_w4a16_stream_t stream);
 
 /* scores */
 enum { MOE_W4A16_SOFTMAX = 0, MOE_W4A16_SIGMOID = 1 };
@@ -573,6 +589,31 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linear_config* c
                                                 const void* w, const float* x_scale, const float* w_scale,
                                                 const float* bias, const void* residual, void* out,
                                                 moe_w4a16_stream_t stream);
+
+typedef struct {
+  int32_t dtype;        /* of the logits: F32, F16 or BF16 */
+  int32_t vocab;        /* V: 1..2^28 */
+  int32_t top_k;        /* k: 0..min(32, V) */
+  int32_t token_bits;   /* of the tokens: 32 or 64 */
+  int64_t ld_logits;
+} moe_w4a16_logprobs_config;
+
+/* Per row t of logits [T][V], with p the softmax of the row:
+ *   logprob[t] = ln p[tokens[t]]
+ *   entropy[t] = -sum_i p_i ln p_i                                   (in nats)
+ *   topk_ids[t][k], topk_logprobs[t][k] = the k largest logits' places, largest
+ *       first (ties: lower place), and their ln p            (NULL for k == 0)
+ * A logit of -inf or NaN is masked: its p is 0 and its ln p -inf.  A row with
+ * fewer than k unmasked logits fills up with the lowest masked places at -inf,
+ * so ids are always distinct and in [0, V).  A row that its mask leaves empty
+ * has entropy 0 and ln p = -inf everywhere.  Logits of +inf share the row's
+ * whole probability.  A token outside [0, V) stands for none: its logprob is 0.
+ * The result of a row does not depend on the other rows of the call but for
+ * the order of its sums, and does not change from run to run. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_token_logprobs(const moe_w4a16_logprobs_config* cfg, int64_t T,
+                                                        const void* logits, const void* tokens, float* logprob,
+                                                        float* entropy, int32_t* topk_ids, float* topk_logprobs,
+                                                        moe_w4a16_stream_t stream);
 
 /* Synchronises the calling thread's current device, reads and clears the
  * status word of the block operators there: OK, or ERR_TIMEOUT if a bounded

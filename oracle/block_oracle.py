@@ -101,3 +101,34 @@ def linear(x, w, x_scale=None, w_scale=None, bias=None, act="none", residual=Non
     if residual is not None:
         out = out + np.asarray(residual, np.float64)
     return out, a, mag
+
+
+def block_scales(v, n=128):
+    """max |v| / 448 of every n values of a row, the last block as long as it is: [T, ceil(H / n)]."""
+    v = np.abs(np.asarray(v, np.float64))
+    return np.stack([v[:, i:i + n].max(-1) for i in range(0, v.shape[1], n)], -1) / 448
+
+
+def token_logprobs(logits, tokens, top_k):
+    """(logprob, entropy, ids, top, spread) in float64; spread: per row (sum p |d|, sum p d^2) of d = x - max."""
+    x = np.asarray(logits, np.float64)
+    T, V = x.shape
+    lp, ent = np.zeros(T), np.zeros(T)
+    ids, top = np.zeros((T, top_k), np.int32), np.zeros((T, top_k))
+    spread = np.zeros((T, 2))
+    for t in range(T):
+        row = np.where(np.isnan(x[t]), -np.inf, x[t])
+        m = row.max()
+        with np.errstate(invalid="ignore"):
+            d = np.where(row == m, 0.0, row - m) if m != -np.inf else np.full(V, -np.inf)
+        e = np.exp(d)
+        s = e.sum()
+        lnp = d - math.log(s) if s > 0 else d
+        fin = e > 0
+        p = e[fin] / s if s > 0 else e[fin]
+        ent[t] = -(p * lnp[fin]).sum()
+        spread[t] = (p * -d[fin]).sum(), (p * d[fin] ** 2).sum()
+        lp[t] = lnp[tokens[t]] if 0 <= tokens[t] < V else 0.0
+        order = np.argsort(-row, kind="stable")[:top_k]
+        ids[t], top[t] = order, lnp[order]
+    return lp, ent, ids, top, spread

@@ -3,10 +3,11 @@
   add_rmsnorm   residual addition + root-mean-square norm (+ an 8-bit copy)
   linear        matrix product with scales, bias, activation and residual
   route_scored  expert ids and weights from router logits
+  token_logprobs  log probabilities of given tokens, entropies, best alternatives
 
-The definitions, limits and masking rules are those of moe_w4a16_add_rmsnorm,
-moe_w4a16_linear and moe_w4a16_route_scored in include/moe_w4a16.h; this
-module and the compiled _block beside it check tensors and marshal pointers.
+The definitions, limits and masking rules are those of the functions of the
+same names (moe_w4a16_...) in include/moe_w4a16.h; this module and the
+compiled _block beside it check tensors and marshal pointers.
 Inputs are CUDA tensors of one device; a wrong shape, type or layout raises
 ValueError, an error of the library MoEError.  Rows may be strided (the last
 dimension contiguous).  There is no backward pass: outputs carry no gradient.
@@ -26,6 +27,7 @@ from . import moe_w4a16 as _m
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5}
+BLOCK = 128   # values that share a scale in the block-scaled operators
 _F32, _I32, _E4M3 = torch.float32, torch.int32, torch.float8_e4m3fn
 
 
@@ -49,6 +51,11 @@ class LinearConfig(ctypes.Structure):
                 ("ld_out", ctypes.c_int64)]
 
 
+class LogprobsConfig(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("vocab", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("token_bits", ctypes.c_int32), ("ld_logits", ctypes.c_int64)]
+
+
 @functools.lru_cache(maxsize=None)
 def _lib():
     lib = _m.load_library()
@@ -56,6 +63,8 @@ def _lib():
     lib.moe_w4a16_add_rmsnorm.argtypes = [vp, i64] + [vp] * 8
     lib.moe_w4a16_route_scored.argtypes = [vp, i64] + [vp] * 5
     lib.moe_w4a16_linear.argtypes = [vp, i64] + [vp] * 8
+    lib.moe_w4a16_add_rmsnorm_blocks.argtypes = [vp, i64] + [vp] * 8
+    lib.moe_w4a16_token_logprobs.argtypes = [vp, i64] + [vp] * 7
     lib.moe_w4a16_block_status.argtypes = []
     lib.moe_w4a16_selftest_linear.argtypes = [vp, i64, vp, vp, vp, ctypes.c_int32, i64, vp]
     return lib
@@ -86,25 +95,35 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def add_rmsnorm(x, residual=None, weight=None, *, eps: float = 1e-6, norm: bool = True, quant: bool = False, out=None,
+def _blocks(n):
+    return -(-n // BLOCK)
+
+
+def add_rmsnorm(x, residual=None, weight=None, *, eps: float = 1e-6, norm: bool = True, quant=False, out=None,
                 stream=None):
     """s = x + residual, n = s / sqrt(mean s^2 + eps) * weight, per row of x [T, H] (fp16 or bf16).
 
     Returns (y, s, q, q_scale): y = n in x's type (None with norm=False), s in
     x's type (None without a residual), q = n / q_scale in E4M3 with one FP32
-    scale per row (both None unless quant).  out: the same four, to be
-    written (None where not returned); s may be x or residual, y may be x."""
+    scale per row (both None unless quant).  quant="blocks": a scale per row
+    and 128 values instead, q_scale [T, ceil(H / 128)], as linear_blocks takes
+    them.  out: the same four, to be written (None where not returned); s may
+    be x or residual, y may be x."""
+    blocks = quant == "blocks"
+    if not blocks and isinstance(quant, str):
+        raise ValueError("quant must be True, False or 'blocks'")
+    quant = bool(quant)
     if out is None:
         dt = x.dtype
         y = _empty(x.shape, dt, x, stream) if norm else None
         s = _empty(x.shape, dt, x, stream) if residual is not None else None
         q = _empty(x.shape, _E4M3, x, stream) if quant else None
-        qs = _empty(x.shape[:1], _F32, x, stream) if quant else None
+        qs = _empty((x.shape[0], _blocks(x.shape[-1])) if blocks else x.shape[:1], _F32, x, stream) if quant else None
     else:
         y, s, q, qs = out
         if (y is None) == norm or (s is None) != (residual is None) or (q is None) == quant or (qs is None) == quant:
             raise ValueError("out must hold (y, s, q, q_scale), None exactly where nothing is returned")
-    (_native or _load()).add_rmsnorm(x, residual, weight, eps, y, s, q, qs, stream)
+    (_native or _load()).add_rmsnorm(x, residual, weight, eps, y, s, q, qs, stream, blocks)
     return y, s, q, qs
 
 
@@ -149,6 +168,27 @@ def linear(x, w, *, bias=None, act: str = "none", residual=None, x_scale=None, w
         raise ValueError("out has another type than out_dtype")
     (_native or _load()).linear(x, w, x_scale, w_scale, bias, residual, out, code, stream)
     return out
+
+
+def token_logprobs(logits, tokens, top_k: int = 0, *, out=None, stream=None):
+    """(logprob [T], entropy [T], top_ids [T, k] int32, top_logprobs [T, k]), fp32, of the softmax of logits [T, V]
+    (fp32, fp16 or bf16).
+
+    logprob is ln p of tokens [T] (int32 or int64; 0 for a token outside the
+    vocabulary, as padding has), entropy in nats; top_ids and top_logprobs, None
+    for top_k = 0, the k most likely tokens, largest first, ties to the lower
+    id.  Logits of -inf or NaN are masked.  out: the same four, to be written."""
+    if out is None:
+        T = logits.shape[0]
+        p, e = _empty((T,), _F32, logits, stream), _empty((T,), _F32, logits, stream)
+        ids = _empty((T, top_k), _I32, logits, stream) if top_k > 0 else None
+        top = _empty((T, top_k), _F32, logits, stream) if top_k > 0 else None
+    else:
+        p, e, ids, top = out
+        if p is None or e is None or (ids is None) != (top_k == 0) or (top is None) != (top_k == 0):
+            raise ValueError("out must hold (logprob, entropy, top_ids, top_logprobs), None exactly where nothing is returned")
+    (_native or _load()).token_logprobs(logits, tokens, p, e, ids, top, top_k, stream)
+    return p, e, ids, top
 
 
 def status() -> int:

@@ -1,5 +1,5 @@
 // Python module _block: tensor checks and pointer marshalling of the block
-// operators (add_rmsnorm, route_scored, linear) in front of the C ABI.  A whole
+// operators (block.py's functions) in front of the C ABI.  A whole
 // call takes the host 2.3-2.7 us; the same checks in Python and ctypes took
 // 11-14 us, several times the GPU time of the smallest calls.  block.py keeps
 // the signatures, defaults and the allocation of outputs.
@@ -137,10 +137,17 @@ PyObject* guarded(F f) {
   }
 }
 
-// (x, residual, weight, eps, y, s, q, q_scale, stream)
+// A contiguous [T, n] tensor; None leaves *p NULL.
+bool dense(const char* name, PyObject* o, int64_t T, int64_t n, at::ScalarType dt, int dev, void** p) {
+  int64_t ld;
+  if (!rows(name, o, T, n, dt, dev, p, &ld)) return false;
+  return !*p || ld == n || bad(name, "must be contiguous");
+}
+
+// (x, residual, weight, eps, y, s, q, q_scale, stream, blocks)
 PyObject* add_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    if (!nargs_ok(n, 9)) return nullptr;
+    if (!nargs_ok(n, 10)) return nullptr;
     const at::Tensor* x = tensor("x", a[0]);
     int dev;
     if (!x || !input("x", *x, &dev)) return nullptr;
@@ -151,6 +158,7 @@ PyObject* add_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     moe_w4a16_rmsnorm_config c = {};
     type_code(dt, &c.dtype);
     c.hidden = (int32_t)H;
+    const bool blocks = a[9] == Py_True;
     void *px, *pr, *pw, *py, *ps, *pq, *pqs;
     moe_w4a16_stream_t st;
     if (!float_arg(a[3], &c.eps) || !rows("x", a[0], T, H, dt, dev, &px, &c.ld_x) ||
@@ -158,10 +166,12 @@ PyObject* add_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !rows("out y", a[4], T, H, dt, dev, &py, &c.ld_y) ||
         !rows("out s", a[5], T, H, dt, dev, &ps, &c.ld_residual_out) ||
         !rows("out q", a[6], T, H, at::kFloat8_e4m3fn, dev, &pq, &c.ld_q) ||
-        !vec("out q_scale", a[7], T, at::kFloat, dev, &pqs) || !stream_arg(a[8], dev, &st))
+        !(blocks ? dense("out q_scale", a[7], T, (H + 127) / 128, at::kFloat, dev, &pqs)
+                 : vec("out q_scale", a[7], T, at::kFloat, dev, &pqs)) ||
+        !stream_arg(a[8], dev, &st))
       return nullptr;
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
-    return finish(moe_w4a16_add_rmsnorm(&c, T, px, pr, pw, ps, py, pq, static_cast<float*>(pqs), st));
+    return finish((blocks ? moe_w4a16_add_rmsnorm_blocks : moe_w4a16_add_rmsnorm)(&c, T, px, pr, pw, ps, py, pq, static_cast<float*>(pqs), st));
   });
 }
 
@@ -231,6 +241,35 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (logits, tokens, logprob, entropy, ids, top, top_k, stream)
+PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (!nargs_ok(n, 8)) return nullptr;
+    const at::Tensor *l = tensor("logits", a[0]), *tk = l ? tensor("tokens", a[1]) : nullptr;
+    int dev;
+    if (!tk || !input("logits", *l, &dev)) return nullptr;
+    const int64_t T = l->size(0), V = l->size(1);
+    const at::ScalarType dt = l->scalar_type(), tt = tk->scalar_type();
+    moe_w4a16_logprobs_config c = {};
+    if (!type_code(dt, &c.dtype) || c.dtype == MOE_W4A16_E4M3) return bad("logits", "must be fp32, fp16 or bf16"), nullptr;
+    if (tt != at::kInt && tt != at::kLong) return bad("tokens", "must be int32 or int64"), nullptr;
+    if (V > INT32_MAX) return bad("logits", "has too long rows"), nullptr;
+    c.vocab = (int32_t)V;
+    c.token_bits = tt == at::kLong ? 64 : 32;
+    void *pl, *pt, *pp, *pe, *pi, *pk;
+    moe_w4a16_stream_t st;
+    if (!int_arg(a[6], &c.top_k) || !rows("logits", a[0], T, V, dt, dev, &pl, &c.ld_logits) ||
+        !vec("tokens", a[1], T, tt, dev, &pt) || !vec("out logprob", a[2], T, at::kFloat, dev, &pp) ||
+        !vec("out entropy", a[3], T, at::kFloat, dev, &pe) ||
+        !dense("out top_ids", a[4], T, c.top_k, at::kInt, dev, &pi) ||
+        !dense("out top_logprobs", a[5], T, c.top_k, at::kFloat, dev, &pk) || !stream_arg(a[7], dev, &st))
+      return nullptr;
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    return finish(moe_w4a16_token_logprobs(&c, T, pl, pt, static_cast<float*>(pp), static_cast<float*>(pe),
+                                           static_cast<int32_t*>(pi), static_cast<float*>(pk), st));
+  });
+}
+
 PyObject* set_error(PyObject*, PyObject* e) {
   Py_INCREF(e);
   Py_XSETREF(g_error, e);
@@ -241,6 +280,7 @@ PyMethodDef methods[] = {
     {"add_rmsnorm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(add_rmsnorm)), METH_FASTCALL, nullptr},
     {"route_scored", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(route_scored)), METH_FASTCALL, nullptr},
     {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear)), METH_FASTCALL, nullptr},
+    {"token_logprobs", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(token_logprobs)), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

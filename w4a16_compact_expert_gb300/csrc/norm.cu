@@ -1,11 +1,13 @@
 // moe_w4a16_add_rmsnorm: s = x + residual, n = s / sqrt(mean s^2 + eps) * w,
-// and n in E4M3 with one scale per row.
+// and n in E4M3 with one scale per row; moe_w4a16_add_rmsnorm_blocks: with one
+// scale per row and 128 values.
 //
 // Bound by memory: per value 2 + 2 bytes read and 2 + 2 (+ 1) written.  A row
 // is read once, its sum stays in registers (FP32) between the one reduction
 // and the stores, and the E4M3 scale needs no second reduction: |n| = |s w| r
 // with the row's positive r = 1/sqrt(...), hence max|n| = r max|s w|, and
-// max|s w| is reduced together with the sum of squares.  What has to be kept
+// max|s w| is reduced together with the sum of squares.  A block of 128 is the
+// windows of 16 neighbouring lanes: its max|n| takes four shuffles.  What has to be kept
 // small is the instruction count (at 28 a value the SMs, not the memory, set
 // the time): values go in pairs through the packed FP32 operations, and a
 // thread has up to 32 of a row, which spreads the row's fixed cost.
@@ -26,6 +28,7 @@ struct NormArgs {
   long long T, ld_x, ld_res, ld_res_out, ld_y, ld_q;
   int H;
   float eps, inv_h;
+  int blocks;   // scales per row (BLK)
 };
 
 // How a row's values are read and written, eight (a window) at a time:
@@ -81,7 +84,7 @@ DEV_INLINE void store_window(const Win<E>& w, E* row, int c0, int H) {
 
 // s = x + res of a thread's V windows, its sum of squares, and with q the
 // largest |s w|.
-template <typename E, int V>
+template <typename E, int V, bool BLK>
 DEV_INLINE void row_sums(const NormArgs& a, const Win<E> (&xv)[V], const Win<E> (&rv)[V], const float2 (&w)[V * 4],
                          float2 (&s)[V * 4], float& ss, float& mx) {
 #pragma unroll
@@ -95,7 +98,7 @@ DEV_INLINE void row_sums(const NormArgs& a, const Win<E> (&xv)[V], const Win<E> 
   for (int i = 0; i < V * 4; ++i) sq = fma2(s[i], s[i], sq);
   ss = sq.x + sq.y;
   mx = 0.f;
-  if (a.q) {   // fmaxf leaves NaN out; n and q carry it
+  if (!BLK && a.q) {   // fmaxf leaves NaN out; n and q carry it
 #pragma unroll
     for (int i = 0; i < V * 4; ++i) {
       const float2 n = mul2(s[i], w[i]);
@@ -129,11 +132,12 @@ DEV_INLINE void reduce_row(float& ss, float& mx, bool want_mx, int nt, int tx, f
 }
 
 // The stores of a row: s, n and q of a thread's windows.
-template <Access A, typename E, int V>
+// BLK: every lane of the warp comes here, also those whose row is not `live`.
+template <Access A, typename E, int V, bool BLK>
 DEV_INLINE void finish_row(const NormArgs& a, E* s_row, E* y_row, uint8_t* q_row, float* scale, const int (&c0)[V],
-                           const float2 (&w)[V * 4], float2 (&s)[V * 4], float ss, float mx) {
+                           const float2 (&w)[V * 4], float2 (&s)[V * 4], float ss, float mx, int nt, bool live) {
   const float r = rsqrtf(fmaf(ss, a.inv_h, a.eps));
-  if (a.res_out) {
+  if (a.res_out && live) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       Win<E> o;
@@ -145,7 +149,7 @@ DEV_INLINE void finish_row(const NormArgs& a, E* s_row, E* y_row, uint8_t* q_row
   const float2 rr = make_float2(r, r);
 #pragma unroll
   for (int i = 0; i < V * 4; ++i) s[i] = mul2(mul2(s[i], rr), w[i]);
-  if (a.y) {
+  if (a.y && live) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       Win<E> o;
@@ -154,7 +158,25 @@ DEV_INLINE void finish_row(const NormArgs& a, E* s_row, E* y_row, uint8_t* q_row
       store_window<A>(o, y_row, c0[i], a.H);
     }
   }
-  if (a.q) {
+  if constexpr (BLK) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float c = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c = fmaxf(c, fmaxf(fabsf(s[i * 4 + j].x), fabsf(s[i * 4 + j].y)));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1)
+        if (o < nt) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, o));   // a row of fewer than 16 threads is one block
+      c *= 1.0f / 448.0f;
+      if (c < 1.17549435e-38f) c = 0.f;
+      const float inv = c > 0.f ? __fdividef(1.0f, c) : 0.f;
+      if (live && c0[i] < a.H && c0[i] % 128 == 0) scale[c0[i] / 128] = c;
+      Win<uint8_t> o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pair_to(o, j, mul2(s[i * 4 + j], make_float2(inv, inv)));
+      if (live) store_window<A>(o, q_row, c0[i], a.H);
+    }
+  } else if (a.q) {
     float c = mx * r * (1.0f / 448.0f);
     if (c < 1.17549435e-38f) c = 0.f;   // below 2^-126 the reciprocal would overflow
     const float inv = c > 0.f ? __fdividef(1.0f, c) : 0.f;
@@ -196,7 +218,7 @@ DEV_INLINE void load_weights(const NormArgs& a, const int (&c0)[V], float2 (&w)[
 // Few rows: a row (short rows: several) per CTA.  V windows of a row per
 // thread; blockDim.x threads per row (a power of two below 32, else a
 // multiple of 32), blockDim.y rows per CTA, MT threads at most.
-template <typename E, Access A, int V, int MT>
+template <typename E, Access A, int V, int MT, bool BLK>
 __global__ void __launch_bounds__(MT) add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float2 part[32];
   const int nt = blockDim.x, tx = threadIdx.x, H = a.H;
@@ -221,11 +243,12 @@ __global__ void __launch_bounds__(MT) add_rmsnorm_kernel(const __grid_constant__
   load_weights<A, E, V>(a, c0, w);
   float2 s[V * 4];
   float ss, mx;
-  row_sums<E, V>(a, xv, rv, w, s, ss, mx);
-  reduce_row(ss, mx, a.q != nullptr, nt, tx, part, threadIdx.y * (nt >> 5));
-  if (live)
-    finish_row<A, E, V>(a, static_cast<E*>(a.res_out) + t * a.ld_res_out, static_cast<E*>(a.y) + t * a.ld_y,
-                        a.q + t * a.ld_q, tx == 0 ? a.q_scale + t : nullptr, c0, w, s, ss, mx);
+  row_sums<E, V, BLK>(a, xv, rv, w, s, ss, mx);
+  reduce_row(ss, mx, !BLK && a.q != nullptr, nt, tx, part, threadIdx.y * (nt >> 5));
+  if (BLK || live)
+    finish_row<A, E, V, BLK>(a, static_cast<E*>(a.res_out) + t * a.ld_res_out, static_cast<E*>(a.y) + t * a.ld_y,
+                             a.q + t * a.ld_q, BLK ? a.q_scale + t * a.blocks : tx == 0 ? a.q_scale + t : nullptr, c0, w,
+                             s, ss, mx, nt, live);
 }
 
 // Many rows: a persistent CTA takes every gridDim.x-th one.  Each thread
@@ -239,7 +262,7 @@ __global__ void __launch_bounds__(MT) add_rmsnorm_kernel(const __grid_constant__
 template <int V>
 constexpr int kStreamThreads = V == 1 ? 1280 : V == 2 ? 1024 : 640;   // per SM, as the registers allow
 
-template <typename E, Access A, int V, int MT>
+template <typename E, Access A, int V, int MT, bool BLK>
 __global__ void __launch_bounds__(MT, kStreamThreads<V> / MT) add_rmsnorm_stream_kernel(
     const __grid_constant__ NormArgs a, int ahead) {
   extern __shared__ __align__(16) uint8_t ring_raw[];   // [ahead + 1][V * (1 or 2)][threads] windows
@@ -306,9 +329,10 @@ __global__ void __launch_bounds__(MT, kStreamThreads<V> / MT) add_rmsnorm_stream
     }
     float2 s[V * 4];
     float ss, mx;
-    row_sums<E, V>(a, xv, rv, w, s, ss, mx);
-    reduce_row(ss, mx, a.q != nullptr, nt, tx, part[flip], 0);   // the other half is free: everyone is past its barrier
-    finish_row<A, E, V>(a, s_row, y_row, q_row, tx == 0 ? a.q_scale + t : nullptr, c0, w, s, ss, mx);
+    row_sums<E, V, BLK>(a, xv, rv, w, s, ss, mx);
+    reduce_row(ss, mx, !BLK && a.q != nullptr, nt, tx, part[flip], 0);   // the other half is free: everyone is past its barrier
+    finish_row<A, E, V, BLK>(a, s_row, y_row, q_row, BLK ? a.q_scale + t * a.blocks : tx == 0 ? a.q_scale + t : nullptr,
+                             c0, w, s, ss, mx, nt, true);
     slot = slot == ahead ? 0 : slot + 1;
     x += step * a.ld_x;
     res += step * a.ld_res;
@@ -326,14 +350,14 @@ int row_threads(int windows, int V) {
   return p;
 }
 
-template <typename E, Access A, int V, int MT>
+template <typename E, Access A, int V, int MT, bool BLK>
 cudaError_t launch_rows(const NormArgs& a, int windows, cudaStream_t st) {
   const int nt = row_threads(windows, V), rows = nt >= 128 ? 1 : 128 / nt;
   const long long grid = (a.T + rows - 1) / rows;
-  return launch_pdl(add_rmsnorm_kernel<E, A, V, MT>, dim3((unsigned)grid), dim3(nt, rows), 0, st, 1, a);
+  return launch_pdl(add_rmsnorm_kernel<E, A, V, MT, BLK>, dim3((unsigned)grid), dim3(nt, rows), 0, st, 1, a);
 }
 
-template <typename E, Access A, int V, int MT>
+template <typename E, Access A, int V, int MT, bool BLK>
 cudaError_t launch_stream(const NormArgs& a, int windows, int num_sms, cudaStream_t st) {
   const int nt = row_threads(windows, V);
   const size_t row = (size_t)V * (a.res ? 2 : 1) * nt * 16, fixed = 1024 + sizeof(float2) * 64;
@@ -343,7 +367,7 @@ cudaError_t launch_stream(const NormArgs& a, int windows, int num_sms, cudaStrea
   const int ahead = per_sm * (4 * row + fixed) <= room ? 3 : 2;
   const size_t smem = (ahead + 1) * row;
   if (per_sm * (long long)(smem + fixed) > (long long)room) per_sm = (long long)(room / (smem + fixed));
-  auto kernel = add_rmsnorm_stream_kernel<E, A, V, MT>;
+  auto kernel = add_rmsnorm_stream_kernel<E, A, V, MT, BLK>;
   const cudaError_t e = opt_in_smem((const void*)kernel, smem + sizeof(float2) * 64);   // the static part counts too
   if (e != cudaSuccess) return e;
   const long long grid = a.T < per_sm * num_sms ? a.T : per_sm * num_sms / 8 * 8;
@@ -353,7 +377,7 @@ cudaError_t launch_stream(const NormArgs& a, int windows, int num_sms, cudaStrea
 // The split of a row over threads.  It follows from H and the alignment (and,
 // for the streaming kernel, from there being enough rows for it), so the same
 // row gives the same bits within each of the two kernels.
-template <typename E, Access A>
+template <typename E, Access A, bool BLK>
 cudaError_t launch_a(const NormArgs& a, int num_sms, cudaStream_t st) {
   const int windows = (a.H + (A == kPeeled ? 14 : 7)) / 8;   // a peeled row of H can touch one more
   if constexpr (A != kSingle) {
@@ -361,24 +385,26 @@ cudaError_t launch_a(const NormArgs& a, int num_sms, cudaStream_t st) {
     // peeled from 16 on (T = 2048, H = 1001: 8.2 and 7.3); short rows go
     // several to a CTA
     if (windows > 96 && a.T >= (A == kAligned ? 4ll : 16ll) * num_sms) {
-      if (windows <= 160) return launch_stream<E, A, 1, 160>(a, windows, num_sms, st);
-      if (windows <= 320) return launch_stream<E, A, 2, 160>(a, windows, num_sms, st);
-      if (windows <= 640) return launch_stream<E, A, 4, 160>(a, windows, num_sms, st);
-      if (windows <= 1280) return launch_stream<E, A, 4, 320>(a, windows, num_sms, st);
-      return launch_stream<E, A, 4, 640>(a, windows, num_sms, st);
+      if (windows <= 160) return launch_stream<E, A, 1, 160, BLK>(a, windows, num_sms, st);
+      if (windows <= 320) return launch_stream<E, A, 2, 160, BLK>(a, windows, num_sms, st);
+      if (windows <= 640) return launch_stream<E, A, 4, 160, BLK>(a, windows, num_sms, st);
+      if (windows <= 1280) return launch_stream<E, A, 4, 320, BLK>(a, windows, num_sms, st);
+      return launch_stream<E, A, 4, 640, BLK>(a, windows, num_sms, st);
     }
   }
-  if (windows <= 256) return launch_rows<E, A, 1, 256>(a, windows, st);
-  if (windows <= 512) return launch_rows<E, A, 1, 512>(a, windows, st);
-  if (windows <= 1024) return launch_rows<E, A, 2, 512>(a, windows, st);
-  return launch_rows<E, A, 5, 512>(a, windows, st);
+  if (windows <= 256) return launch_rows<E, A, 1, 256, BLK>(a, windows, st);
+  if (windows <= 512) return launch_rows<E, A, 1, 512, BLK>(a, windows, st);
+  if (windows <= 1024) return launch_rows<E, A, 2, 512, BLK>(a, windows, st);
+  return launch_rows<E, A, 5, 512, BLK>(a, windows, st);
 }
 
 template <typename E>
 cudaError_t launch_e(const NormArgs& a, Access acc, int num_sms, cudaStream_t st) {
-  return acc == kAligned  ? launch_a<E, kAligned>(a, num_sms, st)
-         : acc == kPeeled ? launch_a<E, kPeeled>(a, num_sms, st)
-                          : launch_a<E, kSingle>(a, num_sms, st);
+  // blocks start at a row's start, not on the grid of a peeled row
+  if (a.blocks) return acc == kAligned ? launch_a<E, kAligned, true>(a, num_sms, st) : launch_a<E, kSingle, true>(a, num_sms, st);
+  return acc == kAligned  ? launch_a<E, kAligned, false>(a, num_sms, st)
+         : acc == kPeeled ? launch_a<E, kPeeled, false>(a, num_sms, st)
+                          : launch_a<E, kSingle, false>(a, num_sms, st);
 }
 
 // Peeled: every tensor in use starts its row t at the same place of the 16-byte
@@ -393,12 +419,9 @@ Access access_of(const NormArgs& a) {
   return (m & 7) == 0 && a.ld_x % 8 == 0 && a.H % 8 == 0 && (!a.w || blk::aligned(a.w, 16)) ? kAligned : kPeeled;
 }
 
-}  // namespace
-
-extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_add_rmsnorm(
-    const moe_w4a16_rmsnorm_config* cfg, int64_t T, const void* x, const void* residual, const void* weight,
-    void* residual_out, void* y, void* q, float* q_scale, moe_w4a16_stream_t stream) try {
-  const char* op = "add_rmsnorm";
+moe_w4a16_status run_norm(const char* op, const moe_w4a16_rmsnorm_config* cfg, int64_t T, const void* x,
+                          const void* residual, const void* weight, void* residual_out, void* y, void* q, float* q_scale,
+                          bool blocks, moe_w4a16_stream_t stream) {
   if (!cfg) return blk::reject(op, "cfg is NULL");
   const moe_w4a16_rmsnorm_config c = *cfg;
   if (c.dtype != MOE_W4A16_F16 && c.dtype != MOE_W4A16_BF16) return blk::reject(op, "dtype must be F16 or BF16");
@@ -412,6 +435,7 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_add_rmsnorm(
   if (T == 0) return MOE_W4A16_OK;
   if (!residual_out && !y && !q) return blk::reject(op, "no output given");
   if (!q != !q_scale) return blk::reject(op, "q and q_scale go together");
+  if (blocks && !q) return blk::reject(op, "q and q_scale are required");
   if (!x) return blk::reject(op, "x is NULL");
   if (!blk::aligned(x, 2) || !blk::aligned(residual, 2) || !blk::aligned(weight, 2) ||
       !blk::aligned(residual_out, 2) || !blk::aligned(y, 2) || !blk::aligned(q_scale, 4))
@@ -426,6 +450,7 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_add_rmsnorm(
   a.q_scale = q_scale;
   a.T = T;
   a.H = c.hidden;
+  a.blocks = blocks ? (c.hidden + 127) / 128 : 0;
   a.eps = c.eps;
   a.inv_h = 1.0f / (float)c.hidden;
   a.ld_x = c.ld_x ? c.ld_x : c.hidden;
@@ -440,6 +465,22 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_add_rmsnorm(
   const cudaError_t e = c.dtype == MOE_W4A16_F16 ? launch_e<__half>(a, acc, num_sms, st)
                                                      : launch_e<__nv_bfloat16>(a, acc, num_sms, st);
   return e == cudaSuccess ? MOE_W4A16_OK : blk::launch_failed(op, e);
+}
+
+}  // namespace
+
+extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_add_rmsnorm(
+    const moe_w4a16_rmsnorm_config* cfg, int64_t T, const void* x, const void* residual, const void* weight,
+    void* residual_out, void* y, void* q, float* q_scale, moe_w4a16_stream_t stream) try {
+  return run_norm("add_rmsnorm", cfg, T, x, residual, weight, residual_out, y, q, q_scale, false, stream);
 } catch (...) {   // the host's heap is full
+  return MOE_W4A16_ERR_OOM;
+}
+
+extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_add_rmsnorm_blocks(
+    const moe_w4a16_rmsnorm_config* cfg, int64_t T, const void* x, const void* residual, const void* weight,
+    void* residual_out, void* y, void* q, float* q_scale, moe_w4a16_stream_t stream) try {
+  return run_norm("add_rmsnorm_blocks", cfg, T, x, residual, weight, residual_out, y, q, q_scale, true, stream);
+} catch (...) {
   return MOE_W4A16_ERR_OOM;
 }

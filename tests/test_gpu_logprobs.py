@@ -2,10 +2,11 @@
 
 Tolerances are error bounds, u = 2^-24.  A term e^d, d = x - max: the
 difference is off by u |d|, the product with log2 e by as much again, the
-exponential by 2 ulp: 4 u |d| + 4 u relative.  The sum S: a thread adds at most
-V / 256 + 32 terms to a sum (two sums, at least 128 threads up to 8192 values,
-512 above), then at most 17 joins of three roundings and a rescaling exponential
-of up to 4 u |d| + 4 u each, where what is rescaled far weighs little:
+exponential by 2 ulp: 4 u |d| + 4 u relative.  The sum S: a thread adds V / 256
+terms to a sum (two sums, 128 threads; one warp, up to 16 terms), with two
+roundings per batch of 16 more, then three joins of six roundings and a
+rescaling exponential of up to 4 u |d| + 4 u each, where what is rescaled far
+weighs little:
   rel(S) <= (V / 256 + 150) u + 8 u D,   D = sum p |d|.
 ln p: rel(S), the logarithm (2 ulp) and two subtractions: 4 u (|ln p| + ln V).
 Entropy ln S - E / S: E's terms carry the same errors with weights p |d|:
@@ -70,7 +71,7 @@ def check(x, tok, k, outs):
 @pytest.mark.parametrize("T,V,k", [(1, 1, 0), (1, 1, 1), (3, 2, 2), (5, 7, 3), (2, 31, 31), (3, 32, 32), (4, 33, 32),
                                    (7, 127, 5), (1, 129, 20), (65, 500, 20), (3, 1000, 1), (700, 1024, 8), (2, 4097, 32),
                                    (1, 8191, 20), (5, 8192, 32), (1, 9001, 32), (33, 16385, 7), (1, 32003, 20), (90, 32003, 5),
-                                   (400, 20000, 4), (1, 50304, 32), (17, 50304, 0), (2, 151936, 20), (1, 262145, 32)])
+                                   (400, 20000, 4), (1300, 500, 16), (1300, 1000, 5), (1300, 3, 2), (1, 50304, 32), (40, 33000, 32), (17, 50304, 0), (2, 151936, 20), (1, 262145, 32)])
 def test_shapes(T, V, k, dtype):
     x, tok = rand(T, V, dtype, V + k), tokens_of(T, V, T)
     check(x, tok, k, B.token_logprobs(x, tok, k))

@@ -456,6 +456,8 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_sim_fail(moe_w4a16_cache* c, int3
  *   moe_w4a16_route_scored  expert ids and weights from router logits:
  *                           softmax or sigmoid scores, a balancing bias,
  *                           groups, top-k, renormalised weights
+ *   moe_w4a16_linear_blocks the matrix product of E4M3 operands with a scale per
+ *                           block of 128 (as checkpoints hold 8-bit weights)
  *   moe_w4a16_add_rmsnorm_blocks  the norm with its 8-bit copy in blocks: a
  *                           scale per row and 128 values
  *   moe_w4a16_token_logprobs  log probabilities of given tokens, entropies and
@@ -591,6 +593,37 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linear_config* c
                                                 moe_w4a16_stream_t stream);
 
 typedef struct {
+  int32_t out_dtype;    /* of out: F16, BF16, F32 or E4M3; the residual has it too */
+  int32_t n;            /* N: output features, 1..2^29 */
+  int32_t k;            /* K: input features, 1..2^24 */
+  int32_t act;          /* MOE_W4A16_ACT_* */
+  int32_t reserved;     /* 0 */
+  int32_t reserved2;    /* 0 */
+  int64_t ld_x, ld_w, ld_x_scale, ld_w_scale, ld_residual, ld_out;
+} moe_w4a16_linear_blocks_config;
+
+/* moe_w4a16_linear for E4M3 operands whose scales are FP32 per block of 128: with
+ * kb = ceil(K / 128) and nb = ceil(N / 128)
+ *   x_scale [T][kb], one per row and 128 of K
+ *   w_scale [nb][kb], one per 128 rows of W and 128 of K; SWIGLU: [2 nb][kb],
+ *           the blocks of the N gate rows, then those of the N up rows (each
+ *           matrix has blocks of its own, also where N is no multiple of 128)
+ *   acc[t][m] = sum_b x_scale[t][b] w_scale[block of m][b] sum_{k in b} x[t][k] W[m][k]
+ *   out[t][n] = act(acc[t][m] + bias[m]) + residual[t][n]
+ * The last blocks may be shorter.  An E4M3 output has a scale per row and 128
+ * values, as x wants it: out_scale[t][j] = max over block j of |o| / 448
+ * ([T][nb], contiguous), out[t][n] = o / out_scale[t][n / 128], of the unrounded
+ * o; a scale below 2^-126 is 0, and so are its values.  It takes no residual.
+ * A block's products accumulate in FP32 on the tensor cores, blocks are scaled
+ * and added in FP32; a call's result does not change from run to run.
+ * Activations, alignment of x and W, aliases and bounded waits are those of
+ * moe_w4a16_linear. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_linear_blocks(const moe_w4a16_linear_blocks_config* cfg, int64_t T,
+                                                       const void* x, const float* x_scale, const void* w,
+                                                       const float* w_scale, const float* bias, const void* residual,
+                                                       void* out, float* out_scale, moe_w4a16_stream_t stream);
+
+typedef struct {
   int32_t dtype;        /* of the logits: F32, F16 or BF16 */
   int32_t vocab;        /* V: 1..2^28 */
   int32_t top_k;        /* k: 0..min(32, V) */
@@ -617,7 +650,7 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_token_logprobs(const moe_w4a16_logprobs
 
 /* Synchronises the calling thread's current device, reads and clears the
  * status word of the block operators there: OK, or ERR_TIMEOUT if a bounded
- * wait of moe_w4a16_linear gave up since the last call (the outputs of that
+ * wait of moe_w4a16_linear or moe_w4a16_linear_blocks gave up since the last call (the outputs of that
  * call are then not valid). */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_block_status(void);
 

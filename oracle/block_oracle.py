@@ -109,6 +109,25 @@ def block_scales(v, n=128):
     return np.stack([v[:, i:i + n].max(-1) for i in range(0, v.shape[1], n)], -1) / 448
 
 
+def spread_scales(scale, rows, cols, block_rows):
+    """[rows][cols] of scales given per block_rows x 128."""
+    s = np.repeat(np.asarray(scale, np.float64), 128, 1)[:, :cols]
+    return s if block_rows == 1 else np.repeat(s, block_rows, 0)[:rows]
+
+
+def linear_blocks(x, w, x_scale, w_scale, bias=None, act="none", residual=None):
+    """linear of x and w times their scales; swiglu: gate and up have blocks of their own."""
+    T, K = x.shape
+    M = w.shape[0]
+    xs = spread_scales(x_scale, T, K, 1)
+    if act == "swiglu":
+        nb = w_scale.shape[0] // 2
+        ws = np.concatenate([spread_scales(w_scale[:nb], M // 2, K, 128), spread_scales(w_scale[nb:], M // 2, K, 128)])
+    else:
+        ws = spread_scales(w_scale, M, K, 128)
+    return linear(np.asarray(x, np.float64) * xs, np.asarray(w, np.float64) * ws, None, None, bias, act, residual)
+
+
 def token_logprobs(logits, tokens, top_k):
     """(logprob, entropy, ids, top, spread) in float64; spread: per row (sum p |d|, sum p d^2) of d = x - max."""
     x = np.asarray(logits, np.float64)

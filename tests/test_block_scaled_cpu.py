@@ -61,7 +61,34 @@ def test_logprobs_refusals(lib, kw, word):
     refused(lib, logprobs(lib, **kw), word)
 
 
+LINEAR = dict(out_dtype=0, n=200, k=256, act=0, reserved=0, reserved2=0, ld_x=0, ld_w=0, ld_x_scale=0, ld_w_scale=0,
+              ld_residual=0, ld_out=0)
+
+
+def linear(lib, T=2, x=P, xs=5 * P, w=2 * P, ws=6 * P, bias=None, res=None, out=3 * P, os=None, **kw):
+    cfg = B.LinearBlocksConfig(**{**LINEAR, **kw})
+    return lib.moe_w4a16_linear_blocks(ctypes.addressof(cfg), T, x, xs, w, ws, bias, res, out, os, None)
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(out_dtype=4), "out_dtype"), (dict(out_dtype=-1), "out_dtype"), (dict(act=6), "activation"),
+    (dict(act=-1), "activation"), (dict(reserved=1), "reserved"), (dict(reserved2=1), "reserved"), (dict(n=0), "n outside"),
+    (dict(k=0), "n outside"), (dict(n=(1 << 29) + 1), "n outside"), (dict(k=(1 << 24) + 16), "n outside"),
+    (dict(T=-1), "T"), (dict(ld_x=255), "stride"), (dict(ld_out=199), "stride"), (dict(ld_residual=1), "stride"),
+    (dict(ld_x_scale=1), "stride"), (dict(ld_w_scale=1), "stride"), (dict(k=264), "16 bytes"), (dict(ld_w=264), "16 bytes"),
+    (dict(ld_x=1 << 41), "too large"), (dict(x=None), "NULL"), (dict(w=None), "NULL"), (dict(out=None), "NULL"),
+    (dict(xs=None), "NULL"), (dict(ws=None), "NULL"), (dict(os=P), "out_scale"), (dict(out_dtype=3), "out_scale"),
+    (dict(out_dtype=3, os=P, res=4 * P), "residual"), (dict(x=P + 8), "aligned"), (dict(w=P + 2), "aligned"),
+    (dict(out=P + 1), "aligned"), (dict(res=P + 1), "aligned"), (dict(bias=P + 2), "aligned"), (dict(xs=P + 2), "aligned"),
+    (dict(ws=P + 2), "aligned"), (dict(out_dtype=3, os=P + 2), "aligned"), (dict(out=P), "alias"), (dict(out=2 * P), "alias"),
+    (dict(out_dtype=3, os=5 * P), "alias"), (dict(out_dtype=3, os=6 * P), "alias")])
+def test_linear_refusals(lib, kw, word):
+    refused(lib, linear(lib, **kw), word)
+
+
 def test_null_configs_and_no_rows(lib):
+    refused(lib, lib.moe_w4a16_linear_blocks(None, 1, P, P, P, P, None, None, P, None, None), "cfg")
+    assert linear(lib, T=0, x=None, xs=None, w=None, ws=None, out=None) == F.OK
     refused(lib, lib.moe_w4a16_add_rmsnorm_blocks(None, 1, P, None, None, None, P, P, P, None), "cfg")
     refused(lib, lib.moe_w4a16_token_logprobs(None, 1, P, P, P, P, P, P, None), "cfg")
     assert norm(lib, T=0, x=None) == F.OK
@@ -93,3 +120,13 @@ def test_oracle_block_scales_by_hand():
     v = np.zeros((1, 130))
     v[0, 5], v[0, 129] = -448.0, 896.0
     assert O.block_scales(v).tolist() == [[1.0, 2.0]]
+
+
+def test_oracle_linear_blocks_by_hand():
+    """One row of ones: block sums of 128 and 2 times their scales; gate and up blocks of their own."""
+    x, w = np.ones((1, 130)), np.ones((2, 130))
+    xs = np.array([[2.0, 3.0]])
+    out, _, _ = O.linear_blocks(x, w, xs, np.array([[0.5, 10.0]]))
+    assert out.tolist() == [[128 * 1.0 + 2 * 30.0] * 2]
+    out, pre, _ = O.linear_blocks(x, w, xs, np.array([[0.5, 10.0], [0.25, 0.0]]), act="swiglu")
+    assert pre.tolist() == [[188.0, 64.0]] and np.allclose(out, 188.0 * 64.0)

@@ -2,6 +2,7 @@
 
   add_rmsnorm   residual addition + root-mean-square norm (+ an 8-bit copy)
   linear        matrix product with scales, bias, activation and residual
+  linear_blocks the same of E4M3 operands with a scale per block of 128
   route_scored  expert ids and weights from router logits
   token_logprobs  log probabilities of given tokens, entropies, best alternatives
 
@@ -51,6 +52,13 @@ class LinearConfig(ctypes.Structure):
                 ("ld_out", ctypes.c_int64)]
 
 
+class LinearBlocksConfig(ctypes.Structure):
+    _fields_ = [("out_dtype", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("reserved2", ctypes.c_int32), ("ld_x", ctypes.c_int64),
+                ("ld_w", ctypes.c_int64), ("ld_x_scale", ctypes.c_int64), ("ld_w_scale", ctypes.c_int64),
+                ("ld_residual", ctypes.c_int64), ("ld_out", ctypes.c_int64)]
+
+
 class LogprobsConfig(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("vocab", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("token_bits", ctypes.c_int32), ("ld_logits", ctypes.c_int64)]
@@ -64,6 +72,7 @@ def _lib():
     lib.moe_w4a16_route_scored.argtypes = [vp, i64] + [vp] * 5
     lib.moe_w4a16_linear.argtypes = [vp, i64] + [vp] * 8
     lib.moe_w4a16_add_rmsnorm_blocks.argtypes = [vp, i64] + [vp] * 8
+    lib.moe_w4a16_linear_blocks.argtypes = [vp, i64] + [vp] * 9
     lib.moe_w4a16_token_logprobs.argtypes = [vp, i64] + [vp] * 7
     lib.moe_w4a16_block_status.argtypes = []
     lib.moe_w4a16_selftest_linear.argtypes = [vp, i64, vp, vp, vp, ctypes.c_int32, i64, vp]
@@ -168,6 +177,32 @@ def linear(x, w, *, bias=None, act: str = "none", residual=None, x_scale=None, w
         raise ValueError("out has another type than out_dtype")
     (_native or _load()).linear(x, w, x_scale, w_scale, bias, residual, out, code, stream)
     return out
+
+
+def linear_blocks(x, w, x_scale, w_scale, *, bias=None, act: str = "none", residual=None, out_dtype=None, out=None,
+                  out_scale=None, stream=None):
+    """act(x w^T + bias) + residual for E4M3 x [T, K] with fp32 x_scale [T, ceil(K / 128)] and E4M3 w [N, K] with
+    fp32 w_scale [ceil(N / 128), ceil(K / 128)], a scale per 128 x 128 block; bias fp32.
+
+    act as in linear; for swiglu w holds N gate rows, then N up rows, and
+    w_scale the blocks of the gate, then those of the up rows.  The output
+    [T, N] has out_dtype (fp16 unless given), fp16, bf16, fp32 like the
+    residual, which it may be, or float8_e4m3fn: then it is returned with its
+    scales [T, ceil(N / 128)] as (out, out_scale), fit to be another call's x
+    and x_scale."""
+    code = _ACTS.get(act)
+    if code is None:
+        raise ValueError("act must be one of " + ", ".join(_ACTS))
+    if out is None:
+        n = w.shape[0] // 2 if code == 5 else w.shape[0]
+        out = _empty((x.shape[0], n), out_dtype or torch.float16, x, stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out has another type than out_dtype")
+    quant = out.dtype is _E4M3
+    if quant and out_scale is None:
+        out_scale = _empty((out.shape[0], _blocks(out.shape[-1])), _F32, x, stream)
+    (_native or _load()).linear_blocks(x, w, x_scale, w_scale, bias, residual, out, out_scale, code, stream)
+    return (out, out_scale) if quant else out
 
 
 def token_logprobs(logits, tokens, top_k: int = 0, *, out=None, stream=None):

@@ -241,6 +241,39 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (x, w, x_scale, w_scale, bias, residual, out, out_scale, act, stream)
+PyObject* linear_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (!nargs_ok(n, 10)) return nullptr;
+    const at::Tensor *x = tensor("x", a[0]), *w = x ? tensor("w", a[1]) : nullptr, *o = w ? tensor("out", a[6]) : nullptr;
+    int dev, wdev;
+    if (!o || !input("x", *x, &dev) || !input("w", *w, &wdev)) return nullptr;
+    const int64_t T = x->size(0), K = x->size(1), M = w->size(0);
+    const at::ScalarType f8 = at::kFloat8_e4m3fn, f32 = at::kFloat, ot = o->scalar_type();
+    moe_w4a16_linear_blocks_config c = {};
+    if (!int_arg(a[8], &c.act)) return nullptr;
+    const bool gated = c.act == MOE_W4A16_ACT_SWIGLU;
+    if (gated && M % 2) return bad("w", "needs an even number of rows for swiglu"), nullptr;
+    const int64_t N = gated ? M / 2 : M, kb = (K + 127) / 128, nb = (N + 127) / 128;
+    if (!type_code(ot, &c.out_dtype)) return bad("the output", "must be fp16, bf16, fp32 or float8_e4m3fn"), nullptr;
+    if (K > INT32_MAX || N > INT32_MAX) return bad("w", "is too large"), nullptr;
+    c.n = (int32_t)N;
+    c.k = (int32_t)K;
+    void *px, *pw, *pxs, *pws, *pb, *pr, *po, *pos;
+    moe_w4a16_stream_t st;
+    if (!rows("x", a[0], T, K, f8, dev, &px, &c.ld_x) || !rows("w", a[1], M, K, f8, dev, &pw, &c.ld_w) ||
+        !rows("x_scale", a[2], T, kb, f32, dev, &pxs, &c.ld_x_scale) ||
+        !rows("w_scale", a[3], gated ? 2 * nb : nb, kb, f32, dev, &pws, &c.ld_w_scale) ||
+        !vec("bias", a[4], M, f32, dev, &pb) || !rows("residual", a[5], T, N, ot, dev, &pr, &c.ld_residual) ||
+        !rows("out", a[6], T, N, ot, dev, &po, &c.ld_out) || !dense("out_scale", a[7], T, nb, f32, dev, &pos) ||
+        !stream_arg(a[9], dev, &st))
+      return nullptr;
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    return finish(moe_w4a16_linear_blocks(&c, T, px, static_cast<float*>(pxs), pw, static_cast<float*>(pws),
+                                          static_cast<float*>(pb), pr, po, static_cast<float*>(pos), st));
+  });
+}
+
 // (logits, tokens, logprob, entropy, ids, top, top_k, stream)
 PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -280,6 +313,7 @@ PyMethodDef methods[] = {
     {"add_rmsnorm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(add_rmsnorm)), METH_FASTCALL, nullptr},
     {"route_scored", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(route_scored)), METH_FASTCALL, nullptr},
     {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear)), METH_FASTCALL, nullptr},
+    {"linear_blocks", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear_blocks)), METH_FASTCALL, nullptr},
     {"token_logprobs", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(token_logprobs)), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -79,6 +79,9 @@ inline size_t never_set_word(int H) { return counter_words(H) - 1; }
 cudaError_t launch_selftest_wait(DevStatus* st, const unsigned* never_set, int which, long long limit,
                                  cudaStream_t s);
 
+// linear_blocks.cu: reads and clears its kernels' status word on the current device.
+cudaError_t take_linear_blocks_status(DevStatus* s);
+
 // repack.cu
 cudaError_t launch_repack_matrix(const uint8_t* q, const uint16_t* s, uint8_t* slot_base,
                                  const MatLayout& m, cudaStream_t st);

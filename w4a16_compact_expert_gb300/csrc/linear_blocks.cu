@@ -33,6 +33,7 @@ struct BlockArgs {
   int kb, nb;     // blocks of K; of the output features
   int xs_vec, ws_vec;   // four neighbouring scales of a row can be read at once
   float* qs;      // scales of an E4M3 output
+  int wide_rows;  // every 32 bytes of a row of the output (and the residual) can be stored at once
 };
 struct E4M3 {
   uint8_t v;
@@ -49,7 +50,7 @@ DEV_INLINE float4 load_scales(const float* row, int k, int kb, int vec) {
 DEV_INLINE float lane4(const float4& f, int i) { return i == 0 ? f.x : i == 1 ? f.y : i == 2 ? f.z : f.w; }
 
 // Waits for the tensor memory loads of this thread; r is not read before.
-DEV_INLINE void wait_ld16(uint32_t (&r)[16]) {
+DEV_INLINE void wait_ld(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
@@ -64,12 +65,16 @@ DEV_INLINE void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-DEV_INLINE float2 pair_at(const uint32_t (&r)[16], int j) {
+template <int N>
+DEV_INLINE float2 pair_at(const uint32_t (&r)[N], int j) {
   return make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
 }
 
-DEV_INLINE void arrive_at(uint32_t bar) {   // cluster address
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrives at a cluster address.  Nothing but tensor memory changes hands, whose
+// reads tcgen05.fence::before_thread_sync has ordered: a release at cluster scope
+// waits for the thread's memory accesses, 1,200 cycles a chunk here.
+DEV_INLINE void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // The MMAs of one K chunk into a fresh accumulator.
@@ -121,7 +126,7 @@ DEV_INLINE void store_e4m3_row(const BlockArgs& b, int t, int n0, int lane, cons
 #pragma unroll
   for (int j = 0; j < 4; j += 2)
     w |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[j] * inv, v[j + 1] * inv), __NV_SATFINITE, __NV_E4M3) << (8 * j);
-  if (a.vec >= 4 && n0 + 4 * lane + 4 <= a.N) {
+  if (a.vec == 4 && n0 + 4 * lane + 4 <= a.N) {
     *reinterpret_cast<uint32_t*>(out) = w;
   } else {
 #pragma unroll
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__(192, 2)
       for (int g = 0; g < P * NT / 16; ++g) {
         uint32_t v[16];
         tmem_ld16(d + (uint32_t)(g * 16), v);
-        wait_ld16(v);
+        wait_ld(v);
         if (g == P * NT / 16 - 1) {
           tc_fence_before();
           __syncwarp();
@@ -378,7 +383,11 @@ struct WideCfg {
   static constexpr int kStages = 192 * 1024 / kStage > 6 ? 6 : 192 * 1024 / kStage;
   static constexpr int kEpiWarps = 8;
   static constexpr int kTurn = 32 * 32 * 4;   // per epilogue warp: 32 rows x 32 FP32 columns
-  static constexpr int kBars = 2 * kStages + 5;
+  // Accumulators.  From a chunk's commit until the next MMAs into the same columns
+  // pass some 900 cycles (wake up, read and add, arrive, wake up); 256 columns
+  // have room for two only, whose MMAs take 512.
+  static constexpr int kAccs = BN == 256 ? 2 : 4;
+  static constexpr int kBars = 2 * kStages + 2 * kAccs + 1;
   static constexpr int kSmem = kStages * kStage + kEpiWarps * kTurn + kBars * 8 + 16 + 1024;
   // Warp 0 loads, warp 1 multiplies, warps 4-11 add up and finish.  Three warps
   // share a scheduler's 16384 registers, 168 each at launch; the first warpgroup
@@ -388,41 +397,95 @@ struct WideCfg {
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
-// A thread's kF features of a token (its sums are in tensor memory) to E4M3 with
+// 32 bytes of a row, loaded and stored at once: full sectors, whatever the rows'
+// distance.
+DEV_INLINE void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+DEV_INLINE void load32(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+
+// The end of the epilogue for a thread's 16 gate and 16 up sums of a token, the
+// features from n on.  A lane stores its own row, in whole 32-byte sectors
+// (2048 tokens, [11264][2048]: 50 us; turned first, as other outputs are, 54.
+// Without the gate the two are as fast, and with few columns turning is faster).
+template <typename O>
+DEV_INLINE void finish_rows(const LinearArgs& a, const uint32_t (&s)[2][16], int t, int n) {
+  constexpr int kWords = 16 * (int)sizeof(O) / 4, kPer = 4 / (int)sizeof(O);
+  float v[16], u[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    v[i] = __uint_as_float(s[0][i]);
+    u[i] = __uint_as_float(s[1][i]);
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      v[i] += a.bias[n + i];
+      u[i] += a.bias[a.N + n + i];
+    }
+  }
+  if (t >= a.T) return;
+  union {
+    uint32_t w[kWords / 8][8];
+    O o[16];
+  } x;
+  if (a.res) {
+#pragma unroll
+    for (int i = 0; i < kWords / 8; ++i)
+      load32(static_cast<const O*>(a.res) + (size_t)t * a.ld_res + n + i * 8 * kPer, x.w[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    x.o[i] = blk::from_float<O>(silu(v[i]) * u[i] + (a.res ? blk::to_float(x.o[i]) : 0.f));
+#pragma unroll
+  for (int i = 0; i < kWords / 8; ++i) store32(static_cast<O*>(a.out) + (size_t)t * a.ld_out + n + i * 8 * kPer, x.w[i]);
+}
+
+// A thread's kF features of a token (the sums are in tensor memory) to E4M3 with
 // the scale of their block, which a thread has whole (kF = 128) or shares with
 // the same lane of the quarter's other warp: first the features' values back
 // into the place of their (gate) sums and the largest, then scaled and stored.
 template <bool GATED, int kF, typename Column>
 DEV_INLINE void finish_e4m3(const BlockArgs& b, uint32_t d, Column column, int t, int n0, float* row_max, int h, int q) {
+  static_assert(kF == 64 || kF == 128, "one or two warps to a block");
   const LinearArgs& a = b.a;
   const int lane = threadIdx.x & 31;
   float m = 0.f;
 #pragma unroll 1
   for (int c = 0; c < kF; c += 16) {
+    const int n = n0 + c;
     uint32_t g[16], w[16];
     tmem_ld16(d + column(c), g);
     if (GATED) tmem_ld16(d + column(kF + c), w);
-    wait_ld16(g);
-    if (GATED) wait_ld16(w);
+    wait_ld(g);
+    if (GATED) wait_ld(w);
     float v[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      v[j] = __uint_as_float(g[j]);
-      if (a.bias) v[j] += a.bias[min(n0 + c + j, a.N - 1)];
+    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(g[j]);
+    if (a.bias) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] += a.bias[min(n + j, a.N - 1)];
     }
     if constexpr (GATED) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        float u = __uint_as_float(w[j]);
-        if (a.bias) u += a.bias[a.N + min(n0 + c + j, a.N - 1)];
-        v[j] = silu(v[j]) * u;
+        float up = __uint_as_float(w[j]);
+        if (a.bias) up += a.bias[a.N + min(n + j, a.N - 1)];
+        v[j] = silu(v[j]) * up;
       }
     } else {
       activate(v, a.act);
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      if (n0 + c + j >= a.N) v[j] = 0.f;
+      if (n + j >= a.N) v[j] = 0.f;
       m = fmaxf(m, fabsf(v[j]));   // NaN is left out, its value carries it
       g[j] = __float_as_uint(v[j]);
     }
@@ -441,24 +504,30 @@ DEV_INLINE void finish_e4m3(const BlockArgs& b, uint32_t d, Column column, int t
   if (live && n0 < a.N && (kF == 128 || h == 0)) b.qs[(size_t)t * b.nb + n0 / 128] = s;
   uint8_t* out = static_cast<uint8_t*>(a.out) + (size_t)t * a.ld_out + n0;
 #pragma unroll 1
-  for (int c = 0; c < kF && n0 + c < a.N; c += 16) {
-    uint32_t g[16], w[4];
-    tmem_ld16(d + column(c), g);
-    wait_ld16(g);
+  for (int c = 0; c < kF && n0 + c < a.N; c += 32) {
+    uint32_t g[2][16], w[8];
+    tmem_ld16(d + column(c), g[0]);
+    tmem_ld16(d + column(c + 16), g[1]);
+    wait_ld(g[0]);
+    wait_ld(g[1]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 lo = make_float2(__uint_as_float(g[4 * j]) * inv, __uint_as_float(g[4 * j + 1]) * inv);
-      const float2 hi = make_float2(__uint_as_float(g[4 * j + 2]) * inv, __uint_as_float(g[4 * j + 3]) * inv);
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t* p = &g[j / 4][4 * (j % 4)];
+      const float2 lo = make_float2(__uint_as_float(p[0]) * inv, __uint_as_float(p[1]) * inv);
+      const float2 hi = make_float2(__uint_as_float(p[2]) * inv, __uint_as_float(p[3]) * inv);
       w[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
              (uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16;
     }
     if (!live) continue;
-    if (a.vec == 16 && n0 + c + 16 <= a.N) {
-      *reinterpret_cast<uint4*>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (b.wide_rows && n0 + c + 32 <= a.N) {
+      store32(out + c, w);
     } else {
+#pragma unroll 1
+      for (int j = 0; j < 32 && n0 + c + j < a.N; ++j) {
+        out[c + j] = (uint8_t)w[0];
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (n0 + c + j < a.N) out[c + j] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+        for (int i = 0; i < 8; ++i) w[i] = __funnelshift_r(w[i], i < 7 ? w[i + 1] : 0u, 8);
+      }
     }
   }
 }
@@ -469,9 +538,9 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
                               const __grid_constant__ CUtensorMap tmX) {
   using C = WideCfg<BN>;
   constexpr bool QUANT = std::is_same<O, E4M3>::value;
-  constexpr uint32_t kCols = 2 * BN;         // two accumulators
+  constexpr uint32_t kCols = C::kAccs * BN;
   constexpr int FT = GATED ? BN / 2 : BN;    // output features per tile
-  constexpr int kW = BN / 2;                 // sums of a thread; GATED: of kW / 2 gate columns, then of their up columns
+  constexpr int kW = BN / 2;                 // sums of a thread; GATED: of kF gate columns, then of their up columns
   constexpr int kF = GATED ? kW / 2 : kW;    // features of a thread
   static_assert(!QUANT || FT % 128 == 0, "a block of the output lies in a tile");
   const LinearArgs& a = b.a;
@@ -481,9 +550,9 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
   float* row_max = turn;   // E4M3 outputs, which are not turned: the halves' largest values, [tile's parity][half][128]
   uint64_t* full = reinterpret_cast<uint64_t*>(turn + C::kEpiWarps * (C::kTurn / 4));
   uint64_t* empty = full + C::kStages;
-  uint64_t* acc_full = empty + C::kStages;   // [2]
-  uint64_t* acc_empty = acc_full + 2;        // [2]
-  uint64_t* last = acc_empty + 2;            // every MMA of the pair is done
+  uint64_t* acc_full = empty + C::kStages;
+  uint64_t* acc_empty = acc_full + C::kAccs;
+  uint64_t* last = acc_empty + C::kAccs;   // every MMA of the pair is done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(last + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
@@ -499,7 +568,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < C::kAccs; ++s) {
       mbar_init(&acc_full[s], 1);
       mbar_init(&acc_empty[s], 2 * C::kEpiWarps);
     }
@@ -523,30 +592,29 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
-    Pipe p;
-    bool ok = true;
-    int issued = 0;
-    const uint32_t leader = elect_lane(), ring = smem_u32(smem), bars = smem_u32(full), bars0 = map_to_rank(full, 0);
-    for (int tile = first; tile < tiles && ok; tile += step) {
-      const int m0 = (tile % mtiles) * 256 + rank * 128, n0 = tile / mtiles * FT;
-      const int b0 = rank == 0 ? n0 : GATED ? a.N + n0 : n0 + BN / 2;   // this CTA's weight rows
-      for (int k = 0; k < nk; ++k) {
-        if (!mbar_wait_bounded(&empty[p.i], p.ph ^ 1u, &g_block_status)) {
-          ok = false;
-          break;
+      Pipe p;
+      bool ok = true;
+      int issued = 0;
+      const uint32_t leader = elect_lane(), ring = smem_u32(smem), bars = smem_u32(full), bars0 = map_to_rank(full, 0);
+      for (int tile = first; tile < tiles && ok; tile += step) {
+        const int m0 = (tile % mtiles) * 256 + rank * 128, n0 = tile / mtiles * FT;
+        const int b0 = rank == 0 ? n0 : GATED ? a.N + n0 : n0 + BN / 2;   // this CTA's weight rows
+        for (int k = 0; k < nk; ++k) {
+          if (!mbar_wait_bounded(&empty[p.i], p.ph ^ 1u, &g_block_status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = ring + (uint32_t)(p.i * C::kStage), bar0 = bars0 + (uint32_t)(p.i * 8);
+          if (rank == 0) expect_bytes(bars + (uint32_t)(p.i * 8), (uint32_t)(2 * C::kStage), leader);
+          fetch<2>(dst, &tmX, k * 128, m0, bar0, leader);
+          fetch<2>(dst + C::kA, &tmW, k * 128, b0, bar0, leader);
+          ++issued;
+          p.next(C::kStages);
         }
-        const uint32_t dst = ring + (uint32_t)(p.i * C::kStage), bar0 = bars0 + (uint32_t)(p.i * 8);
-        if (rank == 0) expect_bytes(bars + (uint32_t)(p.i * 8), (uint32_t)(2 * C::kStage), leader);
-        fetch<2>(dst, &tmX, k * 128, m0, bar0, leader);
-        fetch<2>(dst + C::kA, &tmW, k * 128, b0, bar0, leader);
-        ++issued;
-        p.next(C::kStages);
       }
-    }
-    wait_released<C::kStages>(empty, issued);
-    __syncwarp();
-  } else if (warp == 1 && rank == 0) {
-    {
+      wait_released<C::kStages>(empty, issued);
+      __syncwarp();
+    } else if (warp == 1 && rank == 0) {
       Pipe p, acc;
       bool ok = true;
       const uint32_t leader = elect_lane();
@@ -566,13 +634,12 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
           commit_pair(&empty[p.i], 3, leader);
           commit_pair(&acc_full[acc.i], 3, leader);
           p.next(C::kStages);
-          acc.next(2);
+          acc.next(C::kAccs);
         }
       commit_pair(last, 1, leader);
       mbar_wait_bounded(last, 0, &g_block_status);
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     // a TMEM lane (token) per thread; the two warps of a lane quarter share the columns
@@ -586,10 +653,10 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     int parity = 0;
     for (int tile = first; tile < tiles && ok; tile += step, parity ^= 1) {
       const int t0 = (tile % mtiles) * 256 + rank * 128 + q * 32, n0 = tile / mtiles * FT + h * kF;   // this warp's
-      const float* xs = b.xs + (size_t)min(t0 + lane, a.T - 1) * b.ld_xs;
       const int blk = min(n0 / 128, b.nb - 1);
+      const float* xs = b.xs + (size_t)min(t0 + lane, a.T - 1) * b.ld_xs;
       const float* ws = b.ws + (size_t)blk * b.ld_ws;
-      const float* wu = b.ws + (size_t)(blk + b.nb) * b.ld_ws;
+      const float* wu = b.ws + (size_t)(GATED ? blk + b.nb : blk) * b.ld_ws;   // of the up rows
       float2 sum[kW / 2];
 #pragma unroll
       for (int i = 0; i < kW / 2; ++i) sum[i] = make_float2(0.f, 0.f);
@@ -610,9 +677,13 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
           tc_fence_after();
           const uint32_t d = lanes + (uint32_t)(acc.i * BN);
           const float fg = lane4(sg, i), fu = lane4(su, i);
+          // 16 columns are on their way while 16 are added; the MMAs may have the
+          // accumulator back as soon as the last are read (the last chunk's is
+          // kept for the sums)
+          const bool keep = k + i + 1 == nk;
           uint32_t v[2][16];
           tmem_ld16(d + column(0), v[0]);
-          wait_ld16(v[0]);
+          wait_ld(v[0]);
 #pragma unroll
           for (int g = 0; g < kW / 16; ++g) {
             if (g + 1 < kW / 16) tmem_ld16(d + column(16 * g + 16), v[(g + 1) & 1]);
@@ -620,14 +691,14 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               sum[g * 8 + j] = blk::fma2(pair_at(v[g & 1], j), make_float2(f, f), sum[g * 8 + j]);
-            if (g + 1 < kW / 16) wait_ld16(v[(g + 1) & 1]);
+            if (g + 1 < kW / 16) wait_ld(v[(g + 1) & 1]);
+            if (g + 2 == kW / 16 && !keep) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) arrive_at(empty0 + (uint32_t)(acc.i * 8));
+            }
           }
-          if (k + i + 1 < nk) {   // the last chunk's accumulator is kept for the sums
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_at(empty0 + (uint32_t)(acc.i * 8));
-            acc.next(2);
-          }
+          if (!keep) acc.next(C::kAccs);
         }
       }
       if (!ok) break;
@@ -643,39 +714,44 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
         tmem_st16(d + column(16 * g), v);
       }
       tmem_wait_st();
-      if (t0 < a.T && (n0 < a.N || QUANT)) {   // the same for the whole warp (QUANT: for both of a quarter)
+      if (t0 < a.T) {   // the same for a lane quarter
         if constexpr (QUANT) {
           finish_e4m3<GATED, kF>(b, d, column, t0 + lane, n0, row_max + parity * 256, h, q);
         } else {
           constexpr int kStep = GATED ? 16 : 32, kLanes = kStep / 4;
-          Four cb = {};
-          const int cl = GATED ? lane & 15 : lane, up = GATED && lane >= 16 ? a.N : 0;
-          if (a.bias && cl < kF / 4) {   // as finish_turned wants them
-            const int cn = n0 + cl / kLanes * kStep;
-            const bool wide = a.vec == 4 && cn + kStep <= a.N;
-            cb = load_columns(a, a.bias + up, cn + cl % kLanes * (wide ? 4 : 1), wide ? 1 : kLanes);
-          }
+          const bool direct = GATED && b.wide_rows && n0 + kF <= a.N;
 #pragma unroll 1
           for (int c = 0; c < kF && n0 + c < a.N; c += kStep) {
+            const int n = n0 + c;
             uint32_t v[2][16];
             tmem_ld16(d + column(c), v[0]);
             tmem_ld16(d + column(GATED ? kF + c : c + 16), v[1]);
-            wait_ld16(v[0]);
-            wait_ld16(v[1]);
+            wait_ld(v[0]);
+            wait_ld(v[1]);
+            if (direct) {
+              if constexpr (GATED) finish_rows<O>(a, v, t0 + lane, n);
+            } else {
+              Four cb = {};   // as finish_turned wants them
+              const int cl = GATED ? lane & 15 : lane, up = GATED && lane >= 16 ? a.N : 0;
+              if (a.bias && cl < kLanes) {
+                const bool wide = a.vec == 4 && n + kStep <= a.N;
+                cb = load_columns(a, a.bias + up, n + cl * (wide ? 4 : 1), wide ? 1 : kLanes);
+              }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(buf + lane * 32 + ((j ^ (lane & 7)) * 4)) =
-                  make_uint4(v[j / 4][4 * (j % 4)], v[j / 4][4 * (j % 4) + 1], v[j / 4][4 * (j % 4) + 2], v[j / 4][4 * (j % 4) + 3]);
-            __syncwarp();
-            finish_turned<GATED, O>(a, buf, t0, n0 + c, lane, Four{}, cb, c / kStep);
-            __syncwarp();
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(buf + lane * 32 + ((j ^ (lane & 7)) * 4)) =
+                    make_uint4(v[j / 4][4 * (j % 4)], v[j / 4][4 * (j % 4) + 1], v[j / 4][4 * (j % 4) + 2], v[j / 4][4 * (j % 4) + 3]);
+              __syncwarp();
+              finish_turned<GATED, O>(a, buf, t0, n, lane, Four{}, cb, 0);
+              __syncwarp();
+            }
           }
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_at(empty0 + (uint32_t)(acc.i * 8));
-      acc.next(2);
+      acc.next(C::kAccs);
     }
   }
   tc_fence_before();
@@ -863,8 +939,7 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear_blocks(const moe_w4a1
   a.act = c.act;
   a.idesc = 1u << 4;   // FP32 accumulator; kind::f8f6f4 0 = E4M3
   const size_t vb = 4 * (size_t)os;
-  if (quant) a.vec = blk::aligned(out, 16) && ld_out % 16 == 0 ? 16 : blk::aligned(out, 4) && ld_out % 4 == 0 ? 4 : 1;
-  else a.vec = blk::aligned(out, vb) && ld_out % 4 == 0 && (!residual || (blk::aligned(residual, vb) && ld_res % 4 == 0)) ? 4 : 1;
+  a.vec = blk::aligned(out, vb) && ld_out % 4 == 0 && (!residual || (blk::aligned(residual, vb) && ld_res % 4 == 0)) ? 4 : 1;
   a.give_up = 0;
   a.limit = 0;
   b.xs = x_scale;
@@ -876,6 +951,8 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear_blocks(const moe_w4a1
   b.xs_vec = kb % 4 == 0 && ld_xs % 4 == 0 && blk::aligned(x_scale, 16);
   b.ws_vec = kb % 4 == 0 && ld_ws % 4 == 0 && blk::aligned(w_scale, 16);
   b.qs = out_scale;
+  b.wide_rows = blk::aligned(out, 32) && ld_out * os % 32 == 0 &&
+                (!residual || (blk::aligned(residual, 32) && ld_res * os % 32 == 0));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = gated ? launch_gated<true>(p, st) : launch_gated<false>(p, st);
   return e == cudaSuccess ? MOE_W4A16_OK : blk::launch_failed(op, e);

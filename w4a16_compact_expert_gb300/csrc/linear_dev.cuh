@@ -422,7 +422,7 @@ constexpr int kMaxDevices = 64;
 // Asked about below in the place of the kernels of its shape, never launched:
 // for a kernel that allocates tensor memory the occupancy query answers one
 // CTA per SM, whatever it allocates.
-static __global__ void __launch_bounds__(320) shape_kernel() {}
+static __global__ void __launch_bounds__(640) shape_kernel() {}
 
 // Clusters of CTAs of this shape that can be resident at once.  GPCs hold a
 // whole number of clusters: at one CTA per SM 76 of 2 but 36 of 4, at two 152 of

@@ -254,17 +254,25 @@ class MoEBlock:
     Returns (out, s); the next block adds them up.  layer: a MoELayer with
     experts and slot table set.  router_w fp16 [E, H]; shared: None or
     (gate_up, down) with gate_up [2 Is, H] in fp16, or in E4M3 with
-    shared_scale fp32 [2 Is], and down fp16 [H, Is].  route: the keyword
-    arguments of route_scored.  The layer's rule on streams (one stream per
-    handle, or ordered by events) is the block's."""
+    shared_scale fp32 [2 Is], and down fp16 [H, Is].  Or both in E4M3 with a
+    scale per 128 x 128 block: shared_scale = (that of gate_up, that of down) as
+    linear_blocks takes them; the norm and the gated product then write E4M3
+    with a scale per 128 values.  route: the keyword arguments of route_scored.
+    The layer's rule on streams (one stream per handle, or ordered by events)
+    is the block's."""
 
     def __init__(self, layer, norm_weight, router_w, shared=None, shared_scale=None, eps: float = 1e-6, **route):
         self.layer, self.norm_weight, self.router_w, self.eps, self.route = layer, norm_weight, router_w, eps, route
         self.gate_up, self.down = shared if shared is not None else (None, None)
         self.scale = shared_scale
+        self.blocks = isinstance(shared_scale, (tuple, list))
         self.quant = self.gate_up is not None and self.gate_up.dtype is _E4M3
         if self.quant != (shared_scale is not None):
             raise ValueError("shared_scale goes with an E4M3 gate_up")
+        if self.blocks:
+            if len(shared_scale) != 2:
+                raise ValueError("shared_scale in blocks is a pair, of gate_up and of down")
+            self.quant = "blocks"
 
     def __call__(self, x, residual=None, stream=None):
         n, s, q, qs = add_rmsnorm(x, residual, self.norm_weight, eps=self.eps, quant=self.quant, stream=stream)
@@ -272,7 +280,10 @@ class MoEBlock:
         ids, w = route_scored(logits, self.layer.cfg.top_k, stream=stream, **self.route)
         out = _empty(n.shape, n.dtype, n, stream)
         self.layer.forward_routed(n, ids, w, out=out, stream=stream)
-        if self.gate_up is not None:
+        if self.blocks:
+            h, hs = linear_blocks(q, self.gate_up, qs, self.scale[0], act="swiglu", out_dtype=_E4M3, stream=stream)
+            linear_blocks(h, self.down, hs, self.scale[1], residual=out, out=out, stream=stream)
+        elif self.gate_up is not None:
             h = linear(q if self.quant else n, self.gate_up, act="swiglu", x_scale=qs, w_scale=self.scale, stream=stream)
             linear(h, self.down, residual=out, out=out, stream=stream)
         return out, x if s is None else s

@@ -86,7 +86,8 @@ DEV_INLINE void multiply_chunk(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id
 }
 
 // ------------------------------------------------------------------ narrow
-template <bool GATED, int NT>
+// PER: CTAs that share an SM.
+template <bool GATED, int NT, int PER>
 struct NarrowCfg {
   static constexpr int P = GATED ? 2 : 1;
   static constexpr int kA = P * 128 * kChunk, kB = NT * kChunk, kStage = kA + kB;
@@ -94,7 +95,7 @@ struct NarrowCfg {
   static constexpr int kRecv = (NT + 7) * P * 128 * 4;
   static constexpr bool kOwnRecv = kRecv <= 24 * 1024 && !GATED;   // else over the stages
   static constexpr int kScales = 4 * 2 * P * NT * 4;   // per multiplying-out warp: two chunks' scales of the tokens
-  static constexpr int kBudget = 110 * 1024;           // two CTAs per SM
+  static constexpr int kBudget = PER == 2 ? 110 * 1024 : 73 * 1024;
   static constexpr int kStages = (kBudget - (kOwnRecv ? kRecv : 0) - kScales) / kStage;
   static constexpr int kRing = kStages * kStage;
   static_assert(kStages >= 2 && (kOwnRecv || kRecv <= kRing), "the parts fit over the stages");
@@ -104,7 +105,7 @@ struct NarrowCfg {
   static constexpr int kSmem = kBarAt + (2 * kStages + 5) * 8 + 16 + 1024;
   static constexpr uint32_t kCols = 2 * P * NT < 32 ? 32 : 2 * P * NT;
   static constexpr int kThreads = 192;   // warp 0 loads, warp 1 multiplies, warps 2-5 add up
-  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(PER * (kSmem + 1024) <= 228 * 1024, "they fit");
 };
 
 // One token's 128 features of a tile, four to a lane: scaled, rounded to E4M3
@@ -135,11 +136,11 @@ DEV_INLINE void store_e4m3_row(const BlockArgs& b, int t, int n0, int lane, cons
   }
 }
 
-template <bool GATED, int NT>
-__global__ void __launch_bounds__(192, 2)
+template <bool GATED, int NT, int PER>
+__global__ void __launch_bounds__(192, PER)
     linear_blocks_narrow_kernel(const __grid_constant__ BlockArgs b, const __grid_constant__ CUtensorMap tmW,
                                 const __grid_constant__ CUtensorMap tmX, int out_dtype, int S, int prefetch) {
-  using C = NarrowCfg<GATED, NT>;
+  using C = NarrowCfg<GATED, NT, PER>;
   constexpr int P = C::P;
   const LinearArgs& a = b.a;
   extern __shared__ uint8_t smem_raw[];
@@ -771,17 +772,35 @@ struct Problem {
   int out_dtype, num_sms, dev;
 };
 
-template <bool GATED, int NT>
-cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
-  using C = NarrowCfg<GATED, NT>;
+template <bool GATED, int NT, int PER>
+cudaError_t launch_narrow_s(const Problem& p, int S, cudaStream_t st) {
+  using C = NarrowCfg<GATED, NT, PER>;
   const LinearArgs& a = p.b.a;
   CUtensorMap mw, mx;
   if (!encode_rows(&mw, p.w, GATED ? 2ll * a.N : a.N, a.K, 1, p.ld_w, 128) ||
       !encode_rows(&mx, p.x, a.T, a.K, 1, p.ld_x, NT))
     return cudaErrorInvalidValue;
-  auto kernel = linear_blocks_narrow_kernel<GATED, NT>;
+  auto kernel = linear_blocks_narrow_kernel<GATED, NT, PER>;
   const cudaError_t e = opt_in_smem((const void*)kernel, C::kSmem);
   if (e != cudaSuccess) return e;
+  const int tiles = (a.N + 127) / 128;
+  const int prefetch = tiles * S > p.num_sms;   // as linear_narrow_kernel
+  return launch_pdl(kernel, dim3((unsigned)(tiles * S)), dim3(C::kThreads), C::kSmem, st, S, p.b, mw, mx, p.out_dtype, S,
+                    prefetch);
+}
+
+// Fewer tiles than SMs are split over clusters.  With more, one CTA to a tile, and
+// for up to 16 tokens three to an SM, which evens out what is left in the last
+// round (T = 8, W [50304][2048], 393 tiles: 18.4 us, two to an SM 22.1, clusters
+// of two 24.9; T = 1, W [28672][8192] 37.0, 37.8, 40.8).
+template <bool GATED, int NT>
+cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
+  using C = NarrowCfg<GATED, NT, 2>;
+  const int tiles = (p.b.a.N + 127) / 128;
+  if (tiles >= p.num_sms) {
+    if constexpr (!GATED && NT == 16) return launch_narrow_s<GATED, NT, 3>(p, 1, st);
+    return launch_narrow_s<GATED, NT, 2>(p, 1, st);
+  }
   // asked once per device; racing first calls ask twice and store the same
   static std::atomic<int> known[kMaxDevices][2][9];
   int fit[2][9];
@@ -795,10 +814,7 @@ cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
         known[p.dev][two][s].store(n, std::memory_order_relaxed);
       }
     }
-  const int tiles = (a.N + 127) / 128, S = split_of(tiles, p.b.kb, fit[0], fit[1]);
-  const int prefetch = tiles * S > p.num_sms;   // as linear_narrow_kernel
-  return launch_pdl(kernel, dim3((unsigned)(tiles * S)), dim3(C::kThreads), C::kSmem, st, S, p.b, mw, mx, p.out_dtype, S,
-                    prefetch);
+  return launch_narrow_s<GATED, NT, 2>(p, split_of(tiles, p.b.kb, fit[0], fit[1]), st);
 }
 
 template <bool GATED, int BN, typename O>
@@ -836,20 +852,23 @@ cudaError_t launch_wide(const Problem& p, cudaStream_t st) {
 }
 
 // The tile width of the wide kernel: rounds of tiles over the resident clusters
-// times a tile's time.  An E4M3 output's block of 128 features has to lie in a
-// tile.
+// times a tile's time, a K chunk 0.42, 0.29 or 0.19 us at 256, 128 or 64 weight
+// rows and the end of a tile 3, 1.5 or 0.8 us, in units of 10 ns.  Measured with
+// 256 / 128 / 64 rows: T = 512, N = K = 2048 12.8 / 9.2 / 7.0 us, T = 2048, N =
+// 4096 28 / 33 / 34, SWIGLU N = 5632 50 / 64 / 83.  An E4M3 output's block of 128
+// features has to lie in a tile.
 template <bool GATED>
 int wide_rows(const Problem& p) {
   const LinearArgs& a = p.b.a;
   const long long slots = p.num_sms / 2;
-  const int rows[3] = {256, 128, 64}, chunk[3] = {58, 34, 28}, fixed[3] = {520, 340, 240};
+  const int rows[3] = {256, 128, 64}, chunk[3] = {42, 29, 19}, end[3] = {300, 150, 80};
   int best = 0;
   long long cost = -1;
   for (int i = 0; i < 3; ++i) {
     const int ft = GATED ? rows[i] / 2 : rows[i];
     if (p.out_dtype == MOE_W4A16_E4M3 && ft < 128) continue;
     const long long tiles = (long long)((a.T + 255) / 256) * ((a.N + ft - 1) / ft);
-    const long long c = (tiles + slots - 1) / slots * p.b.kb * chunk[i] + fixed[i];
+    const long long c = (tiles + slots - 1) / slots * (p.b.kb * (long long)chunk[i] + end[i]);
     if (cost < 0 || c < cost) {
       cost = c;
       best = rows[i];
@@ -862,7 +881,9 @@ template <bool GATED>
 cudaError_t launch_gated(const Problem& p, cudaStream_t st) {
   if (p.b.a.T <= 16) return launch_narrow<GATED, 16>(p, st);
   if (p.b.a.T <= 32) return launch_narrow<GATED, 32>(p, st);
-  if (p.b.a.T <= 64) return launch_narrow<GATED, 64>(p, st);
+  // 64 tokens, SWIGLU [11264][2048]: 13.6 us, the wide kernel 12.1; 48 12.3 and 12.2;
+  // without the gate, W [4096][4096] 9.7 and 9.7, [2048][5632] 8.0 and 11.3
+  if (p.b.a.T <= (GATED ? 48 : 64)) return launch_narrow<GATED, 64>(p, st);
   const int rows = wide_rows<GATED>(p);
   return rows == 256   ? launch_wide<GATED, 256>(p, st)
          : rows == 128 ? launch_wide<GATED, 128>(p, st)

@@ -8,18 +8,24 @@
 // being multiplied into another.  A thread's tensor memory lane is a token
 // (wide kernel), whose scale it needs once per chunk and 128 columns.
 //
-// linear_blocks_narrow_kernel (up to 64 tokens, bound by reading W once): as
-// linear_narrow_kernel, W as the 128-row operand, the K chunks of a tile dealt
-// to the CTAs of a cluster, parts added by a token's owner in rank order.  A
-// tile holds 128 features (SWIGLU: 128 gate and 128 up rows in two
-// accumulators), one block of scales of the output.
+// linear_blocks_narrow_kernel (up to 64 tokens, 48 with SWIGLU; bound by reading W
+// once): as linear_narrow_kernel, W as the 128-row operand, the K chunks of a tile
+// dealt to the CTAs of a cluster, parts added by a token's owner in rank order.  A
+// tile holds 128 features (SWIGLU: 128 gate and 128 up rows in two accumulators),
+// one block of scales of the output.  8 tokens through W [50304][2048] take 18.4 us
+// (5.6 TB/s), one through SWIGLU [11264][2048] 5.9, 8 through [2048][5632] 5.8: the
+// last two lie on the time of a launch and one trip through the pipeline.
 //
-// linear_blocks_wide_kernel (more tokens, bound by the tensor cores): as
-// linear_wide_kernel, CTA pairs over tiles of 256 tokens x BN weight rows.  The
-// two accumulators alternate between chunks instead of tiles.  At a tile's end
-// the sums go back into the last chunk's accumulator, so that the rest of the
-// epilogue is a loop over columns: out of registers it has to be unrolled, and
-// its instructions no longer fit the cache.
+// linear_blocks_wide_kernel (more tokens): as linear_wide_kernel, CTA pairs over
+// tiles of 256 tokens x BN weight rows, but the accumulators (two of 256 columns,
+// four of fewer) go round by chunks instead of tiles.  What bounds it is the adding,
+// not the tensor cores: a chunk's MMAs take 512 cycles at 256 columns, waking up for
+// its accumulator, reading, adding and handing it back 820 (the packed FP32 FMAs
+// alone 270).  At a tile's end the sums go back into the last chunk's accumulator,
+// so that the rest of the epilogue is a loop over columns: out of registers it has to
+// be unrolled, and its instructions no longer fit the cache.  2048 tokens through
+// SWIGLU [11264][2048] to E4M3 take 51 us (1.9 PFLOP/s), 4096 through [2048][5632]
+// to FP16 47 (2.0 PFLOP/s), a residual added 54.
 #include "linear_dev.cuh"
 
 namespace {
@@ -388,7 +394,7 @@ struct WideCfg {
   // pass some 900 cycles (wake up, read and add, arrive, wake up); 256 columns
   // have room for two only, whose MMAs take 512.
   static constexpr int kAccs = BN == 256 ? 2 : 4;
-  static constexpr int kBars = 2 * kStages + 2 * kAccs + 1;
+  static constexpr int kBars = 2 * kStages + 2 * kAccs + 4 + 1;
   static constexpr int kSmem = kStages * kStage + kEpiWarps * kTurn + kBars * 8 + 16 + 1024;
   // Warp 0 loads, warp 1 multiplies, warps 4-11 add up and finish.  Three warps
   // share a scheduler's 16384 registers, 168 each at launch; the first warpgroup
@@ -453,8 +459,12 @@ DEV_INLINE void finish_rows(const LinearArgs& a, const uint32_t (&s)[2][16], int
 // the scale of their block, which a thread has whole (kF = 128) or shares with
 // the same lane of the quarter's other warp: first the features' values back
 // into the place of their (gate) sums and the largest, then scaled and stored.
+// The two warps meet at `pair`, a wait with a limit as all of them: a named barrier
+// would wait for ever for a warp that gave up.  Where it runs out the status says
+// so, and the values of the tile count for nothing.
 template <bool GATED, int kF, typename Column>
-DEV_INLINE void finish_e4m3(const BlockArgs& b, uint32_t d, Column column, int t, int n0, float* row_max, int h, int q) {
+DEV_INLINE void finish_e4m3(const BlockArgs& b, uint32_t d, Column column, int t, int n0, float* row_max, int h, int q,
+                            uint64_t* pair, int parity) {
   static_assert(kF == 64 || kF == 128, "one or two warps to a block");
   const LinearArgs& a = b.a;
   const int lane = threadIdx.x & 31;
@@ -495,7 +505,10 @@ DEV_INLINE void finish_e4m3(const BlockArgs& b, uint32_t d, Column column, int t
   tmem_wait_st();
   if (kF < 128) {
     row_max[h * 128 + q * 32 + lane] = m;
-    asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(pair);
+    mbar_wait_bounded(pair, (uint32_t)parity, &g_block_status);
+    __syncwarp();
     m = fmaxf(m, row_max[(h ^ 1) * 128 + q * 32 + lane]);
   }
   float s = m * (1.f / 448.f);
@@ -553,7 +566,8 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
   uint64_t* acc_empty = acc_full + C::kAccs;
-  uint64_t* last = acc_empty + C::kAccs;   // every MMA of the pair is done
+  uint64_t* pairs = acc_empty + C::kAccs;   // [lane quarter] of its two warps, for E4M3 outputs
+  uint64_t* last = pairs + 4;               // every MMA of the pair is done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(last + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
@@ -573,6 +587,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
       mbar_init(&acc_full[s], 1);
       mbar_init(&acc_empty[s], 2 * C::kEpiWarps);
     }
+    for (int q = 0; q < 4; ++q) mbar_init(&pairs[q], 2);
     mbar_init(last, 1);
     fence_mbar_init();
   }
@@ -651,8 +666,8 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     auto column = [&](int i) { return (uint32_t)(GATED ? (i < kF ? h * kF + i : BN / 2 + h * kF + i - kF) : h * kW + i); };
     Pipe acc;
     bool ok = true;
-    int parity = 0;
-    for (int tile = first; tile < tiles && ok; tile += step, parity ^= 1) {
+    int parity = 0;   // of the tiles finished to E4M3
+    for (int tile = first; tile < tiles && ok; tile += step) {
       const int t0 = (tile % mtiles) * 256 + rank * 128 + q * 32, n0 = tile / mtiles * FT + h * kF;   // this warp's
       const int blk = min(n0 / 128, b.nb - 1);
       const float* xs = b.xs + (size_t)min(t0 + lane, a.T - 1) * b.ld_xs;
@@ -717,7 +732,8 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
       tmem_wait_st();
       if (t0 < a.T) {   // the same for a lane quarter
         if constexpr (QUANT) {
-          finish_e4m3<GATED, kF>(b, d, column, t0 + lane, n0, row_max + parity * 256, h, q);
+          finish_e4m3<GATED, kF>(b, d, column, t0 + lane, n0, row_max + parity * 256, h, q, &pairs[q], parity);
+          parity ^= 1;
         } else {
           constexpr int kStep = GATED ? 16 : 32, kLanes = kStep / 4;
           const bool direct = GATED && b.wide_rows && n0 + kF <= a.N;

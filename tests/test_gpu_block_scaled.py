@@ -400,3 +400,22 @@ def test_quantised_feed_forward(T):
     keep = f64(res)
     got = B.linear_blocks(h, down[:, :I], hs, ds, residual=res, out=res)
     check_linear(h, down[:, :I], hs, ds, None, None, "none", got, r_in=keep)
+
+
+@pytest.mark.parametrize("T,N,act", [(100, 272, "none"), (97, 144, "swiglu"), (257, 403, "none"), (70, 300, "swiglu"),
+                                     (129, 31, "none"), (300, 129, "swiglu"), (66, 260, "gelu")])
+def test_linear_e4m3_rows_of_any_layout(T, N, act):
+    """The same bits whatever the distance and alignment of the output's rows, and nothing written beside them."""
+    t = make_linear(T, N, 400, act, True, seed=N)
+    want = None
+    for ld, off in ((-(-N // 32) * 32, 0), (N, 0), (N + 16, 16), (N + 4 - N % 4, 4), (N + 1, 1), (N + 7, 3), (N + 36, 36)):
+        buf = torch.full(((T + 2) * ld + 64,), 3.0, device="cuda").to(E4)
+        o = buf[ld + off:].as_strided((T, N), (ld, 1))
+        _, s = run(t, act, out=o)
+        got = o.contiguous().view(torch.uint8)
+        if want is None:
+            want = (got, s)
+            check_linear(*t, act, (o, s))
+        assert torch.equal(got, want[0]) and torch.equal(s, want[1])
+        o.view(torch.uint8).fill_(buf[:1].view(torch.uint8)[0])
+        assert (buf.float() == 3).all()

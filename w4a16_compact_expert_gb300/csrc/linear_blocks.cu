@@ -455,6 +455,20 @@ DEV_INLINE void finish_rows(const LinearArgs& a, const uint32_t (&s)[2][16], int
   for (int i = 0; i < kWords / 8; ++i) store32(static_cast<O*>(a.out) + (size_t)t * a.ld_out + n + i * 8 * kPer, x.w[i]);
 }
 
+// Up to 32 rows of up to 32 bytes from `turn` (9 words a row), by a warp.  A call:
+// inlined, it makes the other columns' loop slower (4096^3 76 us instead of 73).
+__device__ __noinline__ void store_bytes(const uint32_t* turn, uint8_t* at, long long ld, int rows, int cols, bool words) {
+  const int lane = threadIdx.x & 31;
+  if (words && cols >= 32) {
+    const int f = lane % 8;
+#pragma unroll 2
+    for (int r = lane / 8; r < rows; r += 4) *reinterpret_cast<uint32_t*>(at + r * ld + 4 * f) = turn[r * 9 + f];
+  } else if (lane < cols) {
+#pragma unroll 2
+    for (int r = 0; r < rows; ++r) at[r * ld + lane] = reinterpret_cast<const uint8_t*>(turn)[r * 36 + lane];
+  }
+}
+
 // A thread's kF features of a token (the sums are in tensor memory) to E4M3 with
 // the scale of their block, which a thread has whole (kF = 128) or shares with
 // the same lane of the quarter's other warp: first the features' values back
@@ -463,8 +477,8 @@ DEV_INLINE void finish_rows(const LinearArgs& a, const uint32_t (&s)[2][16], int
 // would wait for ever for a warp that gave up.  Where it runs out the status says
 // so, and the values of the tile count for nothing.
 template <bool GATED, int kF, typename Column>
-DEV_INLINE void finish_e4m3(const BlockArgs& b, uint32_t d, Column column, int t, int n0, float* row_max, int h, int q,
-                            uint64_t* pair, int parity) {
+DEV_INLINE void finish_e4m3(const BlockArgs& b, uint32_t d, Column column, int t, int n0, float* row_max,
+                            uint32_t* turn, int h, int q, uint64_t* pair, int parity) {
   static_assert(kF == 64 || kF == 128, "one or two warps to a block");
   const LinearArgs& a = b.a;
   const int lane = threadIdx.x & 31;
@@ -532,16 +546,18 @@ DEV_INLINE void finish_e4m3(const BlockArgs& b, uint32_t d, Column column, int t
       w[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
              (uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16;
     }
-    if (!live) continue;
     if (b.wide_rows && n0 + c + 32 <= a.N) {
-      store32(out + c, w);
+      if (live) store32(out + c, w);
     } else {
-#pragma unroll 1
-      for (int j = 0; j < 32 && n0 + c + j < a.N; ++j) {
-        out[c + j] = (uint8_t)w[0];
+      // other rows are turned, so that the lanes of a store lie side by side, in
+      // words or in bytes (T = 2274, N = 5328, K = 112: 18 us, each lane its own
+      // row's bytes 115; T = 333, N = 4001, K = 1424: 10.7 and 27)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __funnelshift_r(w[i], i < 7 ? w[i + 1] : 0u, 8);
-      }
+      for (int j = 0; j < 8; ++j) turn[lane * 9 + j] = w[j];
+      __syncwarp();
+      store_bytes(turn, static_cast<uint8_t*>(a.out) + (size_t)(t - lane) * a.ld_out + n0 + c, a.ld_out,
+                  min(32, a.T - t + lane), a.N - n0 - c, a.vec == 4);
+      __syncwarp();
     }
   }
 }
@@ -557,11 +573,14 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
   constexpr int kW = BN / 2;                 // sums of a thread; GATED: of kF gate columns, then of their up columns
   constexpr int kF = GATED ? kW / 2 : kW;    // features of a thread
   static_assert(!QUANT || FT % 128 == 0, "a block of the output lies in a tile");
+  static_assert(2 * 256 * 4 <= C::kTurn / 2 && 32 * 9 * 4 <= C::kTurn / 2, "both fit");
   const LinearArgs& a = b.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float* turn = reinterpret_cast<float*>(smem + C::kStages * C::kStage);
-  float* row_max = turn;   // E4M3 outputs, which are not turned: the halves' largest values, [tile's parity][half][128]
+  // E4M3 outputs, which turn in the second half of a warp's place: the halves'
+  // largest values, [tile's parity][half][128], in the first
+  float* row_max = turn;
   uint64_t* full = reinterpret_cast<uint64_t*>(turn + C::kEpiWarps * (C::kTurn / 4));
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
@@ -732,7 +751,8 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
       tmem_wait_st();
       if (t0 < a.T) {   // the same for a lane quarter
         if constexpr (QUANT) {
-          finish_e4m3<GATED, kF>(b, d, column, t0 + lane, n0, row_max + parity * 256, h, q, &pairs[q], parity);
+          finish_e4m3<GATED, kF>(b, d, column, t0 + lane, n0, row_max + parity * 256,
+                                  reinterpret_cast<uint32_t*>(buf) + 512, h, q, &pairs[q], parity);
           parity ^= 1;
         } else {
           constexpr int kStep = GATED ? 16 : 32, kLanes = kStep / 4;

@@ -248,3 +248,18 @@ def test_binding_refuses():
     for k in (33, 65, -1):
         with pytest.raises(F.MoEError):
             B.token_logprobs(x, tok, k)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("T,V,k", [(310, 66001, 6), (620, 64008, 0)])
+def test_long_rows_for_some_rounds_of_ctas(T, V, k, dtype):
+    x, tok = rand(T, V, dtype, V + k), tokens_of(T, V, T)
+    pick = torch.tensor([0, 1, T // 2, T - 2, T - 1], device="cuda")
+    outs = B.token_logprobs(x, tok, k)
+    check(x[pick], tok[pick], k, tuple(None if o is None else o[pick] for o in outs))
+    one = [B.token_logprobs(x[i:i + 1], tok[i:i + 1], k) for i in range(0, T, 37)]   # a row by a cluster
+    for j in range(2):
+        a, b = torch.cat([o[j] for o in one]), outs[j][::37]
+        assert (a - b).abs().max() < 1e-5
+    if k:
+        assert torch.equal(torch.cat([o[2] for o in one]), outs[2][::37])

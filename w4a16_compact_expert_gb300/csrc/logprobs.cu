@@ -627,7 +627,10 @@ cudaError_t launch_nt(const LogprobArgs& a, long long T, int S, cudaStream_t st)
 // rows of 131072 BF16 by 128 / 512 threads 120 / 126 (91 / 94), 512 rows of
 // 5000 7.4 / 10.9 (3.9 / 6.2), 64 rows of 5000 5.3 / 3.6 (2.4 / 2.0).  8192
 // rows of 500 by 32 / 128 threads 22 / 39 (8.9 / 17); with more than 16
-// alternatives a warp's 32 maxima tell too little.
+// alternatives a warp's 32 maxima tell too little.  Some rounds of CTAs of 128
+// threads, four to an SM, end with long rows on a few: 680 rows of 197211 BF16 by
+// 128 / 512 threads 100 / 66 (74 / 55), 900 100 / 80 (75 / 65), 1200 104 / 106
+// (79 / 85), 512 of 65536 26 / 24 (18 / 16), of 32000 17 / 17 (10 / 10).
 template <typename E>
 cudaError_t launch_e(const LogprobArgs& a, long long T, int num_sms, cudaStream_t st) {
   const int windows = (int)(a.V / Win<E>::N) + 1;
@@ -637,7 +640,7 @@ cudaError_t launch_e(const LogprobArgs& a, long long T, int num_sms, cudaStream_
     S *= 2;
   if (S > 1) return launch_nt<E, 512, true>(a, T, S, st);
   if (windows <= 128 && T > 8 * num_sms && a.k <= 16) return launch_nt<E, 32, false>(a, T, 1, st);
-  if (windows >= 512 && T <= 2 * num_sms) return launch_nt<E, 512, false>(a, T, 1, st);
+  if (T <= 2 * num_sms ? windows >= 512 : T <= 6 * num_sms && windows >= 8000) return launch_nt<E, 512, false>(a, T, 1, st);
   return launch_nt<E, 128, false>(a, T, 1, st);
 }
 

@@ -419,3 +419,17 @@ def test_linear_e4m3_rows_of_any_layout(T, N, act):
         assert torch.equal(got, want[0]) and torch.equal(s, want[1])
         o.view(torch.uint8).fill_(buf[:1].view(torch.uint8)[0])
         assert (buf.float() == 3).all()
+
+
+@pytest.mark.parametrize("T", [1, 2, 90])
+def test_outputs_fit_the_next_product_at_any_width(T):
+    """Widths off the 16-byte grid: the E4M3 outputs that a call allocates are taken by the next as they are."""
+    H, I = 300, 203
+    pad = lambda t: torch.nn.functional.pad(t.view(torch.uint8), (0, -t.shape[1] % 16)).view(E4)[:, :t.shape[1]]   # noqa: E731
+    x, w = rand((T, H), F16, 1), rand((H,), F16, 2)
+    _, _, q, qs = B.add_rmsnorm(x, None, w, quant="blocks")
+    _, gu, _, gs, _, _ = make_linear(1, I, H, "swiglu", seed=3)
+    _, down, _, ds, _, _ = make_linear(1, H, I, seed=4)
+    h, hs = B.linear_blocks(q, pad(gu), qs, gs, act="swiglu", out_dtype=E4)
+    check_linear(q, gu, qs, gs, None, None, "swiglu", (h, hs))
+    check_linear(h, down, hs, ds, None, None, "none", B.linear_blocks(h, pad(down), hs, ds))

@@ -108,6 +108,12 @@ def _blocks(n):
     return -(-n // BLOCK)
 
 
+def _empty_rows8(T, n, like, stream):
+    """An E4M3 [T, n] whose rows start on the 16-byte grid, as the next linear_blocks wants its x."""
+    pad = -n % 16
+    return _empty((T, n + pad), _E4M3, like, stream)[:, :n] if pad else _empty((T, n), _E4M3, like, stream)
+
+
 def add_rmsnorm(x, residual=None, weight=None, *, eps: float = 1e-6, norm: bool = True, quant=False, out=None,
                 stream=None):
     """s = x + residual, n = s / sqrt(mean s^2 + eps) * weight, per row of x [T, H] (fp16 or bf16).
@@ -116,7 +122,7 @@ def add_rmsnorm(x, residual=None, weight=None, *, eps: float = 1e-6, norm: bool 
     x's type (None without a residual), q = n / q_scale in E4M3 with one FP32
     scale per row (both None unless quant).  quant="blocks": a scale per row
     and 128 values instead, q_scale [T, ceil(H / 128)], as linear_blocks takes
-    them.  out: the same four, to be written (None where not returned); s may
+    them (rows allocated on the 16-byte grid).  out: the same four, to be written (None where not returned); s may
     be x or residual, y may be x."""
     blocks = quant == "blocks"
     if not blocks and isinstance(quant, str):
@@ -126,7 +132,7 @@ def add_rmsnorm(x, residual=None, weight=None, *, eps: float = 1e-6, norm: bool 
         dt = x.dtype
         y = _empty(x.shape, dt, x, stream) if norm else None
         s = _empty(x.shape, dt, x, stream) if residual is not None else None
-        q = _empty(x.shape, _E4M3, x, stream) if quant else None
+        q = (_empty_rows8(*x.shape, x, stream) if blocks else _empty(x.shape, _E4M3, x, stream)) if quant else None
         qs = _empty((x.shape[0], _blocks(x.shape[-1])) if blocks else x.shape[:1], _F32, x, stream) if quant else None
     else:
         y, s, q, qs = out
@@ -189,13 +195,14 @@ def linear_blocks(x, w, x_scale, w_scale, *, bias=None, act: str = "none", resid
     [T, N] has out_dtype (fp16 unless given), fp16, bf16, fp32 like the
     residual, which it may be, or float8_e4m3fn: then it is returned with its
     scales [T, ceil(N / 128)] as (out, out_scale), fit to be another call's x
-    and x_scale."""
+    and x_scale (rows that are allocated here start on the 16-byte grid)."""
     code = _ACTS.get(act)
     if code is None:
         raise ValueError("act must be one of " + ", ".join(_ACTS))
     if out is None:
         n = w.shape[0] // 2 if code == 5 else w.shape[0]
-        out = _empty((x.shape[0], n), out_dtype or torch.float16, x, stream)
+        out = (_empty_rows8(x.shape[0], n, x, stream) if out_dtype is _E4M3 else
+               _empty((x.shape[0], n), out_dtype or torch.float16, x, stream))
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError("out has another type than out_dtype")
     quant = out.dtype is _E4M3

@@ -112,6 +112,7 @@ struct NarrowCfg {
   static constexpr uint32_t kCols = 2 * P * NT < 32 ? 32 : 2 * P * NT;
   static constexpr int kThreads = 192;   // warp 0 loads, warp 1 multiplies, warps 2-5 add up
   static_assert(PER * (kSmem + 1024) <= 228 * 1024, "they fit");
+  static_assert(PER == 3 || kSmem + 1024 >= 85 * 1024, "in clusters: see WideCfg");
 };
 
 // One token's 128 features of a tile, four to a lane: scaled, rounded to E4M3
@@ -402,6 +403,11 @@ struct WideCfg {
   // which hold up to 128 sums and 32 values on their way.
   static constexpr int kThreads = 128 + kEpiWarps * 32;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  // The CTAs of a pair, and of a narrow kernel's cluster, wait for one another with
+  // tensor memory in hand.  A pair shares no SM with another pair nor with a CTA of
+  // a cluster (two of which have tensor memory enough), so that none of them waits
+  // for what another one holds.
+  static_assert(kSmem + 1024 + 85 * 1024 > 228 * 1024, "alone on an SM but for CTAs without a cluster");
 };
 
 // 32 bytes of a row, loaded and stored at once: full sectors, whatever the rows'

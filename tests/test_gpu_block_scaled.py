@@ -433,3 +433,26 @@ def test_outputs_fit_the_next_product_at_any_width(T):
     h, hs = B.linear_blocks(q, pad(gu), qs, gs, act="swiglu", out_dtype=E4)
     check_linear(q, gu, qs, gs, None, None, "swiglu", (h, hs))
     check_linear(h, down, hs, ds, None, None, "none", B.linear_blocks(h, pad(down), hs, ds))
+
+
+@pytest.mark.parametrize("T,H", [(1, 1), (3, 7), (9, 15), (50, 57), (4, 113), (4, 114), (6, 121), (17, 127), (9, 129),
+                                 (33, 241), (33, 243), (5, 255), (5, 1001), (8, 2047), (4, 4095), (3, 8191), (2, 16383),
+                                 (2433, 777), (2500, 1001), (2440, 2047), (2433, 5121), (2433, 10111), (2433, 16383)])
+def test_norm_rows_off_the_grid(T, H):
+    """Every place of a row on the 16-byte grid; only q elsewhere (the same sums, so the same bits); and all outputs
+    elsewhere (another path, whose sums may have another order)."""
+    for dtype, off, r in ((F16, 0, True), (BF16, 3, False), (F16, 7, True)):
+        x, w = rand((T, H + off), dtype, 1), rand((H,), dtype, 3)
+        x = x.view(-1)[off:off + T * H].view(T, H)
+        res = rand((T, H + off), dtype, 2).view(-1)[off:off + T * H].view(T, H) if r else None
+        flat = lambda t: torch.full((T * H + 16,), 3.0, device="cuda").to(t)[off:off + T * H].view(T, H)   # noqa: E731
+        out = (flat(dtype), flat(dtype) if r else None, flat(E4), torch.empty(T, blocks(H), device="cuda"))
+        B.add_rmsnorm(x, res, w, quant="blocks", out=out)
+        pick = sorted({0, 1 % T, 2 % T, 3 % T, 4 % T, 5 % T, 6 % T, 7 % T, T // 2, T - 1})
+        cut = lambda t: None if t is None else t[pick]   # noqa: E731
+        check_norm(x[pick], cut(res), w, 1e-6, [cut(o) for o in out])
+        check_norm(x[pick], cut(res), w, 1e-6, [cut(o) for o in B.add_rmsnorm(x, res, w, quant="blocks")])
+        q = torch.zeros(T, H + 17 - H % 8, device="cuda").to(E4)[:, 1:H + 1]
+        again = B.add_rmsnorm(x, res, w, quant="blocks", out=(flat(dtype), flat(dtype) if r else None, q, torch.empty_like(out[3])))
+        assert torch.equal(out[0], again[0]) and torch.equal(out[3], again[3])
+        assert torch.equal(out[2].view(torch.uint8), again[2].contiguous().view(torch.uint8))

@@ -7,7 +7,8 @@
 // and the stores, and the E4M3 scale needs no second reduction: |n| = |s w| r
 // with the row's positive r = 1/sqrt(...), hence max|n| = r max|s w|, and
 // max|s w| is reduced together with the sum of squares.  A block of 128 is the
-// windows of 16 neighbouring lanes: its max|n| takes four shuffles.  What has to be kept
+// windows of 16 neighbouring lanes: its max|n| takes four shuffles (8192 rows of 4096
+// BF16 with residual 54 us, 5.6 TB/s; a scale per row 54).  What has to be kept
 // small is the instruction count (at 28 a value the SMs, not the memory, set
 // the time): values go in pairs through the packed FP32 operations, and a
 // thread has up to 32 of a row, which spreads the row's fixed cost.
@@ -28,7 +29,8 @@ struct NormArgs {
   long long T, ld_x, ld_res, ld_res_out, ld_y, ld_q;
   int H;
   float eps, inv_h;
-  int blocks;   // scales per row (BLK)
+  int blocks;     // scales per row (BLK)
+  int q_single;   // a peeled row's q lies on another grid (BLK)
 };
 
 // How a row's values are read and written, eight (a window) at a time:
@@ -131,11 +133,14 @@ DEV_INLINE void reduce_row(float& ss, float& mx, bool want_mx, int nt, int tx, f
   }
 }
 
+constexpr int kTops = 160;   // the most windows of a CTA, over 16
+
 // The stores of a row: s, n and q of a thread's windows.
 // BLK: every lane of the warp comes here, also those whose row is not `live`.
 template <Access A, typename E, int V, bool BLK>
 DEV_INLINE void finish_row(const NormArgs& a, E* s_row, E* y_row, uint8_t* q_row, float* scale, const int (&c0)[V],
-                           const float2 (&w)[V * 4], float2 (&s)[V * 4], float ss, float mx, int nt, bool live) {
+                           const float2 (&w)[V * 4], float2 (&s)[V * 4], float ss, float mx, int nt, bool live, float2* top,
+                           int m) {
   const float r = rsqrtf(fmaf(ss, a.inv_h, a.eps));
   if (a.res_out && live) {
 #pragma unroll
@@ -158,7 +163,55 @@ DEV_INLINE void finish_row(const NormArgs& a, E* s_row, E* y_row, uint8_t* q_row
       store_window<A>(o, y_row, c0[i], a.H);
     }
   }
-  if constexpr (BLK) {
+  if constexpr (BLK && A == kPeeled) {
+    // T = 16384, H = 2047 BF16 with residual: 85 us, with q on another grid 90, by
+    // single values 180.  Blocks start with the row, m values into a window, so that the first of 16
+    // neighbouring windows belongs to two: top[b] holds the largest value from m on
+    // in the windows 16 b .. 16 b + 15, and that of the first m in window 16 b + 16.
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int k = i * nt + threadIdx.x, cut = k % 16 == 0 ? m : 0;
+      float own = 0.f, before = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = fabsf(j & 1 ? s[i * 4 + j / 2].y : s[i * 4 + j / 2].x);
+        if (j < cut) before = fmaxf(before, v);
+        else own = fmaxf(own, v);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1)
+        if (o < nt) own = fmaxf(own, __shfl_xor_sync(0xffffffffu, own, o));
+      if (k % 16 == 0) {
+        top[k / 16].x = own;
+        if (k) top[k / 16 - 1].y = before;
+      }
+    }
+    if (nt > 32) __syncthreads();
+    else __syncwarp();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int k = i * nt + threadIdx.x, b = k / 16, cut = k % 16 == 0 ? m : 0;
+      auto scale_of = [&](int at) {
+        const float c = fmaxf(top[at].x, 16 * (at + 1) < V * nt ? top[at].y : 0.f) * (1.0f / 448.0f);
+        return c < 1.17549435e-38f ? 0.f : c;
+      };
+      const float c = scale_of(b), inv = c > 0.f ? __fdividef(1.0f, c) : 0.f;
+      float prev = inv;
+      if (cut > 0 && b > 0) {
+        const float p = scale_of(b - 1);
+        prev = p > 0.f ? __fdividef(1.0f, p) : 0.f;
+      }
+      if (live && k % 16 == 0 && b < a.blocks) scale[b] = c;
+      Win<uint8_t> o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        pair_to(o, j, mul2(s[i * 4 + j], make_float2(2 * j < cut ? prev : inv, 2 * j + 1 < cut ? prev : inv)));
+      if (live) {
+        if (a.q_single) store_window<kSingle>(o, q_row, c0[i], a.H);
+        else store_window<A>(o, q_row, c0[i], a.H);
+      }
+    }
+  } else if constexpr (BLK) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float c = 0.f;
@@ -221,6 +274,7 @@ DEV_INLINE void load_weights(const NormArgs& a, const int (&c0)[V], float2 (&w)[
 template <typename E, Access A, int V, int MT, bool BLK>
 __global__ void __launch_bounds__(MT) add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float2 part[32];
+  __shared__ float2 top[BLK && A == kPeeled ? kTops : 1];
   const int nt = blockDim.x, tx = threadIdx.x, H = a.H;
   const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = t < a.T;
@@ -248,7 +302,7 @@ __global__ void __launch_bounds__(MT) add_rmsnorm_kernel(const __grid_constant__
   if (BLK || live)
     finish_row<A, E, V, BLK>(a, static_cast<E*>(a.res_out) + t * a.ld_res_out, static_cast<E*>(a.y) + t * a.ld_y,
                              a.q + t * a.ld_q, BLK ? a.q_scale + t * a.blocks : tx == 0 ? a.q_scale + t : nullptr, c0, w,
-                             s, ss, mx, nt, live);
+                             s, ss, mx, nt, live, top + threadIdx.y * ((V * nt + 15) / 16), m);
 }
 
 // Many rows: a persistent CTA takes every gridDim.x-th one.  Each thread
@@ -267,6 +321,7 @@ __global__ void __launch_bounds__(MT, kStreamThreads<V> / MT) add_rmsnorm_stream
     const __grid_constant__ NormArgs a, int ahead) {
   extern __shared__ __align__(16) uint8_t ring_raw[];   // [ahead + 1][V * (1 or 2)][threads] windows
   __shared__ float2 part[2][32];
+  __shared__ float2 top[BLK && A == kPeeled ? kTops : 1];   // read before the next row's first barrier, written after it
   const int nt = blockDim.x, tx = threadIdx.x, H = a.H;
   const uint32_t row_bytes = (uint32_t)(V * (a.res ? 2 : 1) * nt * 16);   // of a row in the ring
   const uint32_t mine = smem_u32(ring_raw) + (uint32_t)tx * 16;
@@ -332,7 +387,7 @@ __global__ void __launch_bounds__(MT, kStreamThreads<V> / MT) add_rmsnorm_stream
     row_sums<E, V, BLK>(a, xv, rv, w, s, ss, mx);
     reduce_row(ss, mx, !BLK && a.q != nullptr, nt, tx, part[flip], 0);   // the other half is free: everyone is past its barrier
     finish_row<A, E, V, BLK>(a, s_row, y_row, q_row, BLK ? a.q_scale + t * a.blocks : tx == 0 ? a.q_scale + t : nullptr,
-                             c0, w, s, ss, mx, nt, true);
+                             c0, w, s, ss, mx, nt, true, top, m);
     slot = slot == ahead ? 0 : slot + 1;
     x += step * a.ld_x;
     res += step * a.ld_res;
@@ -360,7 +415,8 @@ cudaError_t launch_rows(const NormArgs& a, int windows, cudaStream_t st) {
 template <typename E, Access A, int V, int MT, bool BLK>
 cudaError_t launch_stream(const NormArgs& a, int windows, int num_sms, cudaStream_t st) {
   const int nt = row_threads(windows, V);
-  const size_t row = (size_t)V * (a.res ? 2 : 1) * nt * 16, fixed = 1024 + sizeof(float2) * 64;
+  const size_t row = (size_t)V * (a.res ? 2 : 1) * nt * 16;
+  const size_t own = sizeof(float2) * (64 + (BLK && A == kPeeled ? kTops : 1)), fixed = 1024 + own;   // the static part
   // three rows ahead where that does not cost a CTA
   const size_t room = 220 * 1024;
   long long per_sm = kStreamThreads<V> / MT * MT / nt;
@@ -368,7 +424,7 @@ cudaError_t launch_stream(const NormArgs& a, int windows, int num_sms, cudaStrea
   const size_t smem = (ahead + 1) * row;
   if (per_sm * (long long)(smem + fixed) > (long long)room) per_sm = (long long)(room / (smem + fixed));
   auto kernel = add_rmsnorm_stream_kernel<E, A, V, MT, BLK>;
-  const cudaError_t e = opt_in_smem((const void*)kernel, smem + sizeof(float2) * 64);   // the static part counts too
+  const cudaError_t e = opt_in_smem((const void*)kernel, smem + own);   // counts too
   if (e != cudaSuccess) return e;
   const long long grid = a.T < per_sm * num_sms ? a.T : per_sm * num_sms / 8 * 8;
   return launch_pdl(kernel, dim3((unsigned)grid), dim3(nt), smem, st, 1, a, ahead);
@@ -400,8 +456,10 @@ cudaError_t launch_a(const NormArgs& a, int num_sms, cudaStream_t st) {
 
 template <typename E>
 cudaError_t launch_e(const NormArgs& a, Access acc, int num_sms, cudaStream_t st) {
-  // blocks start at a row's start, not on the grid of a peeled row
-  if (a.blocks) return acc == kAligned ? launch_a<E, kAligned, true>(a, num_sms, st) : launch_a<E, kSingle, true>(a, num_sms, st);
+  if (a.blocks)
+    return acc == kAligned  ? launch_a<E, kAligned, true>(a, num_sms, st)
+           : acc == kPeeled ? launch_a<E, kPeeled, true>(a, num_sms, st)
+                            : launch_a<E, kSingle, true>(a, num_sms, st);
   return acc == kAligned  ? launch_a<E, kAligned, false>(a, num_sms, st)
          : acc == kPeeled ? launch_a<E, kPeeled, false>(a, num_sms, st)
                           : launch_a<E, kSingle, false>(a, num_sms, st);
@@ -409,13 +467,18 @@ cudaError_t launch_e(const NormArgs& a, Access acc, int num_sms, cudaStream_t st
 
 // Peeled: every tensor in use starts its row t at the same place of the 16-byte
 // (E4M3: 8-byte) grid.
-Access access_of(const NormArgs& a) {
+Access access_of(NormArgs& a) {
   const uintptr_t m = reinterpret_cast<uintptr_t>(a.x) / 2;
   auto same = [&](const void* p, long long ld, int size) {
     return !p || (((reinterpret_cast<uintptr_t>(p) / size - m) & 7) == 0 && ((ld - a.ld_x) & 7) == 0);
   };
-  if (!same(a.res, a.ld_res, 2) || !same(a.res_out, a.ld_res_out, 2) || !same(a.y, a.ld_y, 2) || !same(a.q, a.ld_q, 1))
-    return kSingle;
+  a.q_single = 0;
+  if (!same(a.res, a.ld_res, 2) || !same(a.res_out, a.ld_res_out, 2) || !same(a.y, a.ld_y, 2)) return kSingle;
+  if (!same(a.q, a.ld_q, 1)) {
+    if (!a.blocks) return kSingle;
+    a.q_single = 1;
+    return kPeeled;
+  }
   return (m & 7) == 0 && a.ld_x % 8 == 0 && a.H % 8 == 0 && (!a.w || blk::aligned(a.w, 16)) ? kAligned : kPeeled;
 }
 

@@ -650,8 +650,8 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_token_logprobs(const moe_w4a16_logprobs
 
 /* Synchronises the calling thread's current device, reads and clears the
  * status word of the block operators there: OK, or ERR_TIMEOUT if a bounded
- * wait of moe_w4a16_linear or moe_w4a16_linear_blocks gave up since the last call (the outputs of that
- * call are then not valid). */
+ * wait of moe_w4a16_linear or moe_w4a16_linear_blocks gave up since the last
+ * call (the outputs of that call are then not valid). */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_block_status(void);
 
 /* Failure-detection self-test of moe_w4a16_linear, without a fault: the same
@@ -664,6 +664,16 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_block_status(void);
 MOE_W4A16_API moe_w4a16_status moe_w4a16_selftest_linear(const moe_w4a16_linear_config* cfg, int64_t T, const void* x,
                                                          const void* w, void* out, int32_t which,
                                                          int64_t limit_cycles, moe_w4a16_stream_t stream);
+
+/* The same of moe_w4a16_linear_blocks: T in [1, 16] without an activation or an
+ * E4M3 output, or T above 64 with SWIGLU and an E4M3 output; there which may
+ * also be 3: a warp that adds the products up stops at the end of its first
+ * tile, before it meets the one that shares its blocks of the output. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_selftest_linear_blocks(const moe_w4a16_linear_blocks_config* cfg, int64_t T,
+                                                                const void* x, const float* x_scale, const void* w,
+                                                                const float* w_scale, void* out, float* out_scale,
+                                                                int32_t which, int64_t limit_cycles,
+                                                                moe_w4a16_stream_t stream);
 
 #ifdef __cplusplus
 }

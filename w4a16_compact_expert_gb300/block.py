@@ -76,6 +76,7 @@ def _lib():
     lib.moe_w4a16_token_logprobs.argtypes = [vp, i64] + [vp] * 7
     lib.moe_w4a16_block_status.argtypes = []
     lib.moe_w4a16_selftest_linear.argtypes = [vp, i64, vp, vp, vp, ctypes.c_int32, i64, vp]
+    lib.moe_w4a16_selftest_linear_blocks.argtypes = [vp, i64] + [vp] * 6 + [ctypes.c_int32, i64, vp]
     return lib
 
 
@@ -246,6 +247,21 @@ def selftest_timeout(x, w, which: int, limit_cycles: int) -> None:
     lib = _lib()
     st = lib.moe_w4a16_selftest_linear(ctypes.addressof(cfg), T, _m._ptr(x), _m._ptr(w), _m._ptr(out), int(which),
                                        int(limit_cycles), _m._stream(None))
+    if st != _m.OK:
+        raise _m.MoEError(st, lib.moe_w4a16_last_error(None).decode())
+
+
+def selftest_blocks_timeout(x, w, x_scale, w_scale, which: int, limit_cycles: int) -> None:
+    """The same of linear_blocks (see moe_w4a16_selftest_linear_blocks): up to 16 tokens fp16 out, above 64 swiglu to E4M3."""
+    (T, K), wide = x.shape, x.shape[0] > 64
+    N = w.shape[0] // 2 if wide else w.shape[0]
+    out = torch.empty(T, N, dtype=_E4M3 if wide else torch.float16, device=x.device)
+    out_scale = torch.empty(T, _blocks(N), dtype=_F32, device=x.device) if wide else None
+    cfg = LinearBlocksConfig(out_dtype=3 if wide else 0, n=N, k=K, act=_ACTS["swiglu" if wide else "none"])
+    lib = _lib()
+    st = lib.moe_w4a16_selftest_linear_blocks(ctypes.addressof(cfg), T, _m._ptr(x), _m._ptr(x_scale), _m._ptr(w),
+                                              _m._ptr(w_scale), _m._ptr(out), _m._ptr(out_scale), int(which),
+                                              int(limit_cycles), _m._stream(None))
     if st != _m.OK:
         raise _m.MoEError(st, lib.moe_w4a16_last_error(None).decode())
 

@@ -143,7 +143,7 @@ DEV_INLINE void store_e4m3_row(const BlockArgs& b, int t, int n0, int lane, cons
   }
 }
 
-template <bool GATED, int NT, int PER>
+template <bool GATED, int NT, int PER, bool TEST>
 __global__ void __launch_bounds__(192, PER)
     linear_blocks_narrow_kernel(const __grid_constant__ BlockArgs b, const __grid_constant__ CUtensorMap tmW,
                                 const __grid_constant__ CUtensorMap tmX, int out_dtype, int S, int prefetch) {
@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(192, PER)
     const uint32_t leader = elect_lane(), ring = smem_u32(smem), bars = smem_u32(full);
     int issued = 0;
     for (; issued < mine; ++issued) {
-      if (!mbar_wait_bounded(&empty[p.i], p.ph ^ 1u, &g_block_status)) break;
+      if (TEST && issued == kGiveUpAt && (a.give_up == GIVE_UP_LOADS || (a.give_up == GIVE_UP_ODD_LOADS && (rank & 1)))) break;
+      if (!wait_for<TEST>(&empty[p.i], p.ph ^ 1u, a)) break;
       const int c0 = (rank + issued * S) * 128;
       const uint32_t dst = ring + (uint32_t)(p.i * C::kStage), bar = bars + (uint32_t)(p.i * 8);
       expect_bytes(bar, (uint32_t)C::kStage, leader);
@@ -223,8 +224,9 @@ __global__ void __launch_bounds__(192, PER)
     const uint32_t tm = __reduce_or_sync(0xffffffffu, tmem);   // the same in every lane, and known to be
     const uint64_t desc0 = sw128_desc(smem_u32(smem));
     for (int k = 0; k < mine; ++k) {
-      if (!mbar_wait_bounded(&acc_empty[c.i], c.ph ^ 1u, &g_block_status)) break;
-      if (!mbar_wait_bounded(&full[p.i], p.ph, &g_block_status)) break;
+      if (TEST && k == kGiveUpAt && a.give_up == GIVE_UP_MMA) break;
+      if (!wait_for<TEST>(&acc_empty[c.i], c.ph ^ 1u, a)) break;
+      if (!wait_for<TEST>(&full[p.i], p.ph, a)) break;
       tc_fence_after();
       const uint64_t ad = desc0 + (uint64_t)(p.i * (C::kStage / 16)), bd = ad + C::kA / 16;
 #pragma unroll
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(192, PER)
           if (lane + 32 * i < NT) s[j * NT + lane + 32 * i] = xr[slot][i] * wr[slot][j];
       __syncwarp();
       fetch_scales(slot, k + 2);
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[c.i], c.ph, &g_block_status));
+      ok = __all_sync(0xffffffffu, wait_for<TEST>(&acc_full[c.i], c.ph, a));
       if (!ok) return;
       tc_fence_after();
       const uint32_t d = lanes + (uint32_t)(c.i * P * NT);
@@ -482,7 +484,7 @@ __device__ __noinline__ void store_bytes(const uint32_t* turn, uint8_t* at, long
 // The two warps meet at `pair`, a wait with a limit as all of them: a named barrier
 // would wait for ever for a warp that gave up.  Where it runs out the status says
 // so, and the values of the tile count for nothing.
-template <bool GATED, int kF, typename Column>
+template <bool GATED, int kF, bool TEST, typename Column>
 DEV_INLINE void finish_e4m3(const BlockArgs& b, uint32_t d, Column column, int t, int n0, float* row_max,
                             uint32_t* turn, int h, int q, uint64_t* pair, int parity) {
   static_assert(kF == 64 || kF == 128, "one or two warps to a block");
@@ -527,7 +529,7 @@ DEV_INLINE void finish_e4m3(const BlockArgs& b, uint32_t d, Column column, int t
     row_max[h * 128 + q * 32 + lane] = m;
     __syncwarp();
     if (lane == 0) mbar_arrive(pair);
-    mbar_wait_bounded(pair, (uint32_t)parity, &g_block_status);
+    wait_for<TEST>(pair, (uint32_t)parity, a);
     __syncwarp();
     m = fmaxf(m, row_max[(h ^ 1) * 128 + q * 32 + lane]);
   }
@@ -568,7 +570,7 @@ DEV_INLINE void finish_e4m3(const BlockArgs& b, uint32_t d, Column column, int t
   }
 }
 
-template <bool GATED, int BN, typename O>
+template <bool GATED, int BN, typename O, bool TEST>
 __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     linear_blocks_wide_kernel(const __grid_constant__ BlockArgs b, const __grid_constant__ CUtensorMap tmW,
                               const __grid_constant__ CUtensorMap tmX) {
@@ -641,7 +643,8 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
         const int m0 = (tile % mtiles) * 256 + rank * 128, n0 = tile / mtiles * FT;
         const int b0 = rank == 0 ? n0 : GATED ? a.N + n0 : n0 + BN / 2;   // this CTA's weight rows
         for (int k = 0; k < nk; ++k) {
-          if (!mbar_wait_bounded(&empty[p.i], p.ph ^ 1u, &g_block_status)) {
+          if ((TEST && issued == kGiveUpAt && (a.give_up == GIVE_UP_LOADS || (a.give_up == GIVE_UP_ODD_LOADS && rank))) ||
+              !wait_for<TEST>(&empty[p.i], p.ph ^ 1u, a)) {
             ok = false;
             break;
           }
@@ -664,8 +667,8 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
       const uint64_t desc0 = sw128_desc(smem_u32(smem));
       for (int tile = first; tile < tiles && ok; tile += step)
         for (int k = 0; k < nk; ++k) {
-          if (!mbar_wait_bounded(&acc_empty[acc.i], acc.ph ^ 1u, &g_block_status) ||
-              !mbar_wait_bounded(&full[p.i], p.ph, &g_block_status)) {
+          if ((TEST && k == kGiveUpAt && a.give_up == GIVE_UP_MMA) || !wait_for<TEST>(&acc_empty[acc.i], acc.ph ^ 1u, a) ||
+              !wait_for<TEST>(&full[p.i], p.ph, a)) {
             ok = false;
             break;
           }
@@ -713,7 +716,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
         }
 #pragma unroll 1
         for (int i = 0; i < 4 && k + i < nk; ++i) {
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[acc.i], acc.ph, &g_block_status));
+          ok = __all_sync(0xffffffffu, wait_for<TEST>(&acc_full[acc.i], acc.ph, a));
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = lanes + (uint32_t)(acc.i * BN);
@@ -742,7 +745,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
           if (!keep) acc.next(C::kAccs);
         }
       }
-      if (!ok) break;
+      if (!ok || (TEST && a.give_up == GIVE_UP_FINISH && rank == 0 && warp == 4)) break;
       const uint32_t d = lanes + (uint32_t)(acc.i * BN);
 #pragma unroll
       for (int g = 0; g < kW / 16; ++g) {
@@ -757,7 +760,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
       tmem_wait_st();
       if (t0 < a.T) {   // the same for a lane quarter
         if constexpr (QUANT) {
-          finish_e4m3<GATED, kF>(b, d, column, t0 + lane, n0, row_max + parity * 256,
+          finish_e4m3<GATED, kF, TEST>(b, d, column, t0 + lane, n0, row_max + parity * 256,
                                   reinterpret_cast<uint32_t*>(buf) + 512, h, q, &pairs[q], parity);
           parity ^= 1;
         } else {
@@ -814,7 +817,7 @@ struct Problem {
   int out_dtype, num_sms, dev;
 };
 
-template <bool GATED, int NT, int PER>
+template <bool GATED, int NT, int PER, bool TEST>
 cudaError_t launch_narrow_s(const Problem& p, int S, cudaStream_t st) {
   using C = NarrowCfg<GATED, NT, PER>;
   const LinearArgs& a = p.b.a;
@@ -822,7 +825,7 @@ cudaError_t launch_narrow_s(const Problem& p, int S, cudaStream_t st) {
   if (!encode_rows(&mw, p.w, GATED ? 2ll * a.N : a.N, a.K, 1, p.ld_w, 128) ||
       !encode_rows(&mx, p.x, a.T, a.K, 1, p.ld_x, NT))
     return cudaErrorInvalidValue;
-  auto kernel = linear_blocks_narrow_kernel<GATED, NT, PER>;
+  auto kernel = linear_blocks_narrow_kernel<GATED, NT, PER, TEST>;
   const cudaError_t e = opt_in_smem((const void*)kernel, C::kSmem);
   if (e != cudaSuccess) return e;
   const int tiles = (a.N + 127) / 128;
@@ -835,13 +838,13 @@ cudaError_t launch_narrow_s(const Problem& p, int S, cudaStream_t st) {
 // for up to 16 tokens three to an SM, which evens out what is left in the last
 // round (T = 8, W [50304][2048], 393 tiles: 18.4 us, two to an SM 22.1, clusters
 // of two 24.9; T = 1, W [28672][8192] 37.0, 37.8, 40.8).
-template <bool GATED, int NT>
+template <bool GATED, int NT, bool TEST = false>
 cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
   using C = NarrowCfg<GATED, NT, 2>;
   const int tiles = (p.b.a.N + 127) / 128;
   if (tiles >= p.num_sms) {
-    if constexpr (!GATED && NT == 16) return launch_narrow_s<GATED, NT, 3>(p, 1, st);
-    return launch_narrow_s<GATED, NT, 2>(p, 1, st);
+    if constexpr (!GATED && NT == 16 && !TEST) return launch_narrow_s<GATED, NT, 3, TEST>(p, 1, st);
+    return launch_narrow_s<GATED, NT, 2, TEST>(p, 1, st);
   }
   // asked once per device; racing first calls ask twice and store the same
   static std::atomic<int> known[kMaxDevices][2][9];
@@ -856,10 +859,10 @@ cudaError_t launch_narrow(const Problem& p, cudaStream_t st) {
         known[p.dev][two][s].store(n, std::memory_order_relaxed);
       }
     }
-  return launch_narrow_s<GATED, NT, 2>(p, split_of(tiles, p.b.kb, fit[0], fit[1]), st);
+  return launch_narrow_s<GATED, NT, 2, TEST>(p, split_of(tiles, p.b.kb, fit[0], fit[1]), st);
 }
 
-template <bool GATED, int BN, typename O>
+template <bool GATED, int BN, typename O, bool TEST = false>
 cudaError_t launch_wide_o(const Problem& p, cudaStream_t st) {
   using C = WideCfg<BN>;
   const LinearArgs& a = p.b.a;
@@ -867,7 +870,7 @@ cudaError_t launch_wide_o(const Problem& p, cudaStream_t st) {
   if (!encode_rows(&mw, p.w, GATED ? 2ll * a.N : a.N, a.K, 1, p.ld_w, BN / 2) ||
       !encode_rows(&mx, p.x, a.T, a.K, 1, p.ld_x, 128))
     return cudaErrorInvalidValue;
-  auto kernel = linear_blocks_wide_kernel<GATED, BN, O>;
+  auto kernel = linear_blocks_wide_kernel<GATED, BN, O, TEST>;
   cudaError_t e = opt_in_smem((const void*)kernel, C::kSmem);
   if (e != cudaSuccess) return e;
   static std::atomic<int> resident[kMaxDevices];   // clusters that run at once, asked once per device
@@ -944,12 +947,11 @@ cudaError_t take_linear_blocks_status(DevStatus* s) {
   return e;
 }
 
-extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear_blocks(const moe_w4a16_linear_blocks_config* cfg, int64_t T,
-                                                                  const void* x, const float* x_scale, const void* w,
-                                                                  const float* w_scale, const float* bias,
-                                                                  const void* residual, void* out, float* out_scale,
-                                                                  moe_w4a16_stream_t stream) try {
-  const char* op = "linear_blocks";
+// give_up nonzero: the self-test, with the limit of its waits.
+static moe_w4a16_status run_linear_blocks(const char* op, const moe_w4a16_linear_blocks_config* cfg, int64_t T,
+                                          const void* x, const float* x_scale, const void* w, const float* w_scale,
+                                          const float* bias, const void* residual, void* out, float* out_scale,
+                                          moe_w4a16_stream_t stream, int give_up, int64_t limit) {
   if (!cfg) return blk::reject(op, "cfg is NULL");
   const moe_w4a16_linear_blocks_config c = *cfg;
   if (c.out_dtype < MOE_W4A16_F16 || c.out_dtype > MOE_W4A16_E4M3) return blk::reject(op, "out_dtype must be F16, BF16, F32 or E4M3");
@@ -1003,8 +1005,8 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear_blocks(const moe_w4a1
   a.idesc = 1u << 4;   // FP32 accumulator; kind::f8f6f4 0 = E4M3
   const size_t vb = 4 * (size_t)os;
   a.vec = blk::aligned(out, vb) && ld_out % 4 == 0 && (!residual || (blk::aligned(residual, vb) && ld_res % 4 == 0)) ? 4 : 1;
-  a.give_up = 0;
-  a.limit = 0;
+  a.give_up = give_up;
+  a.limit = limit;
   b.xs = x_scale;
   b.ws = w_scale;
   b.ld_xs = ld_xs;
@@ -1017,8 +1019,36 @@ extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear_blocks(const moe_w4a1
   b.wide_rows = blk::aligned(out, 32) && ld_out * os % 32 == 0 &&
                 (!residual || (blk::aligned(residual, 32) && ld_res * os % 32 == 0));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = gated ? launch_gated<true>(p, st) : launch_gated<false>(p, st);
+  const cudaError_t e = give_up ? (T <= 16 ? launch_narrow<false, 16, true>(p, st) : launch_wide_o<true, 256, E4M3, true>(p, st))
+                        : gated ? launch_gated<true>(p, st)
+                                : launch_gated<false>(p, st);
   return e == cudaSuccess ? MOE_W4A16_OK : blk::launch_failed(op, e);
+}
+
+extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_linear_blocks(const moe_w4a16_linear_blocks_config* cfg, int64_t T,
+                                                                  const void* x, const float* x_scale, const void* w,
+                                                                  const float* w_scale, const float* bias,
+                                                                  const void* residual, void* out, float* out_scale,
+                                                                  moe_w4a16_stream_t stream) try {
+  return run_linear_blocks("linear_blocks", cfg, T, x, x_scale, w, w_scale, bias, residual, out, out_scale, stream, 0, 0);
+} catch (...) {   // the host's heap is full
+  return MOE_W4A16_ERR_OOM;
+}
+
+extern "C" MOE_W4A16_API moe_w4a16_status moe_w4a16_selftest_linear_blocks(
+    const moe_w4a16_linear_blocks_config* cfg, int64_t T, const void* x, const float* x_scale, const void* w,
+    const float* w_scale, void* out, float* out_scale, int32_t which, int64_t limit_cycles,
+    moe_w4a16_stream_t stream) try {
+  const char* op = "selftest_linear_blocks";
+  if (!cfg) return blk::reject(op, "cfg is NULL");
+  if (T < 1 || (T > 16 && T <= 64)) return blk::reject(op, "T outside [1, 16] and (64, 2^30]");
+  if (T <= 16 ? cfg->out_dtype == MOE_W4A16_E4M3 || cfg->act != MOE_W4A16_ACT_NONE
+              : cfg->out_dtype != MOE_W4A16_E4M3 || cfg->act != MOE_W4A16_ACT_SWIGLU)
+    return blk::reject(op, "takes no activation and no E4M3 output up to 16 tokens, SWIGLU and E4M3 above 64");
+  if (which < 0 || which > (T <= 16 ? 2 : 3)) return blk::reject(op, "which outside [0, 2], above 64 tokens [0, 3]");
+  if (limit_cycles < 1000 || limit_cycles > MOE_WAIT_CYCLES) return blk::reject(op, "limit_cycles outside [1000, 2^31]");
+  return run_linear_blocks(op, cfg, T, x, x_scale, w, w_scale, nullptr, nullptr, out, out_scale, stream,
+                           GIVE_UP_MMA + which, limit_cycles);
 } catch (...) {   // the host's heap is full
   return MOE_W4A16_ERR_OOM;
 }

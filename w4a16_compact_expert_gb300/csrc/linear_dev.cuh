@@ -27,7 +27,7 @@ struct LinearArgs {
   int give_up;
   long long limit;
 };
-enum { GIVE_UP_MMA = 1, GIVE_UP_LOADS = 2, GIVE_UP_ODD_LOADS = 3 };
+enum { GIVE_UP_MMA = 1, GIVE_UP_LOADS = 2, GIVE_UP_ODD_LOADS = 3, GIVE_UP_FINISH = 4 };
 constexpr int kGiveUpAt = 2;   // chunks before they stop
 
 // a / (1 + e^-a), relative error up to (2 |a| + 8) 2^-24; 0 where e^-a passes

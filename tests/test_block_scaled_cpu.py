@@ -130,3 +130,24 @@ def test_oracle_linear_blocks_by_hand():
     assert out.tolist() == [[128 * 1.0 + 2 * 30.0] * 2]
     out, pre, _ = O.linear_blocks(x, w, xs, np.array([[0.5, 10.0], [0.25, 0.0]]), act="swiglu")
     assert pre.tolist() == [[188.0, 64.0]] and np.allclose(out, 188.0 * 64.0)
+
+
+@pytest.mark.parametrize("shape", [(8,), (2, 3, 8)])
+def test_norm_in_blocks_refuses_other_dimensions(shape):
+    build_ext.build()
+    with pytest.raises(ValueError):
+        B.add_rmsnorm(torch.zeros(*shape, dtype=torch.float16), quant="blocks")
+
+
+def test_selftest_of_linear_blocks_refuses(lib):
+    def call(T=3, which=0, limit=2000, **kw):
+        cfg = B.LinearBlocksConfig(**{**dict(out_dtype=0, n=128, k=1024, act=0), **kw})
+        return lib.moe_w4a16_selftest_linear_blocks(ctypes.addressof(cfg), T, P, P, P, P, P, None, which, limit, None)
+    refused(lib, call(T=20), "T outside")
+    refused(lib, call(T=0), "T outside")
+    refused(lib, call(which=3), "which")
+    refused(lib, call(limit=10), "limit_cycles")
+    refused(lib, call(act=5), "activation")
+    refused(lib, call(T=70), "activation")
+    refused(lib, call(T=70, act=5, out_dtype=3, which=4), "which")
+    assert lib.moe_w4a16_selftest_linear_blocks(None, 3, P, P, P, P, P, None, 0, 2000, None) == F.ERR_INVALID_ARG

@@ -133,8 +133,9 @@ def add_rmsnorm(x, residual=None, weight=None, *, eps: float = 1e-6, norm: bool 
         dt = x.dtype
         y = _empty(x.shape, dt, x, stream) if norm else None
         s = _empty(x.shape, dt, x, stream) if residual is not None else None
-        q = (_empty_rows8(*x.shape, x, stream) if blocks else _empty(x.shape, _E4M3, x, stream)) if quant else None
-        qs = _empty((x.shape[0], _blocks(x.shape[-1])) if blocks else x.shape[:1], _F32, x, stream) if quant else None
+        rows = blocks and x.dim() == 2   # else refused below
+        q = (_empty_rows8(*x.shape, x, stream) if rows else _empty(x.shape, _E4M3, x, stream)) if quant else None
+        qs = _empty((x.shape[0], _blocks(x.shape[1])) if rows else x.shape[:1], _F32, x, stream) if quant else None
     else:
         y, s, q, qs = out
         if (y is None) == norm or (s is None) != (residual is None) or (q is None) == quant or (qs is None) == quant:

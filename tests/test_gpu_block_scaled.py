@@ -456,3 +456,44 @@ def test_norm_rows_off_the_grid(T, H):
         again = B.add_rmsnorm(x, res, w, quant="blocks", out=(flat(dtype), flat(dtype) if r else None, q, torch.empty_like(out[3])))
         assert torch.equal(out[0], again[0]) and torch.equal(out[3], again[3])
         assert torch.equal(out[2].view(torch.uint8), again[2].contiguous().view(torch.uint8))
+
+
+def test_calls_on_several_streams_at_once():
+    """Products of every form, norms and scores side by side, eagerly and from replayed graphs: each its own result."""
+    jobs = []
+    for i, (T, N, K, act, out) in enumerate(((300, 700, 1024, "swiglu", E4), (2000, 1000, 512, "none", F16), (8, 9000, 1024, "swiglu", E4),
+                                             (60, 3000, 2048, "none", F32), (70, 2000, 640, "swiglu", BF16), (5, 30000, 512, "none", F32),
+                                             (130, 100, 4096, "gelu", E4), (40, 600, 2992, "swiglu", F16))):
+        t = make_linear(T, N, K, act, True, False, out, i)
+        jobs.append(lambda t=t, act=act, out=out: run(t, act, out_dtype=out))
+    x, w = rand((600, 2048), F16, 1), rand((2048,), F16, 2)
+    a, b = rand((100, 4096), F16, 3), rand((3000, 4096), F16, 4, 0.02)
+    lg, tok = rand((90, 40001), BF16, 5), torch.arange(90, device="cuda")
+    jobs += [lambda: B.add_rmsnorm(x, None, w, quant="blocks"), lambda: B.linear(a, b), lambda: B.linear(a[:9], b),
+             lambda: B.token_logprobs(lg, tok, 7)]
+    bits = lambda r: [o.contiguous().view(torch.uint8) for o in (r if isinstance(r, tuple) else (r,)) if o is not None]   # noqa: E731
+    ref = [bits(j()) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    for r in range(6):
+        for i, j in enumerate(jobs):
+            with torch.cuda.stream(streams[(i + r) % 4]):
+                got.append((i, j()))
+    torch.cuda.synchronize()
+    graphs = []
+    for s in streams:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs = [j() for j in jobs]
+        graphs.append((g, outs))
+    for _ in range(3):
+        for s, (g, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    got += [(i, o) for _, outs in graphs for i, o in enumerate(outs)]
+    for i, o in got:
+        assert all(torch.equal(p, q) for p, q in zip(bits(o), ref[i])), i
+    from w4a16_compact_expert_gb300 import moe_w4a16 as F
+    assert B.status() == F.OK

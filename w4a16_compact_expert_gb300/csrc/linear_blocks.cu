@@ -446,12 +446,12 @@ DEV_INLINE void finish_rows(const LinearArgs& a, const uint32_t (&s)[2][16], int
       u[i] += a.bias[a.N + n + i];
     }
   }
-  if (t >= a.T) return;
+  const bool live = t < a.T;
   union {
     uint32_t w[kWords / 8][8];
     O o[16];
-  } x;
-  if (a.res) {
+  } x = {};
+  if (a.res && live) {
 #pragma unroll
     for (int i = 0; i < kWords / 8; ++i)
       load32(static_cast<const O*>(a.res) + (size_t)t * a.ld_res + n + i * 8 * kPer, x.w[i]);
@@ -459,8 +459,11 @@ DEV_INLINE void finish_rows(const LinearArgs& a, const uint32_t (&s)[2][16], int
 #pragma unroll
   for (int i = 0; i < 16; ++i)
     x.o[i] = blk::from_float<O>(silu(v[i]) * u[i] + (a.res ? blk::to_float(x.o[i]) : 0.f));
+  if (live) {
 #pragma unroll
-  for (int i = 0; i < kWords / 8; ++i) store32(static_cast<O*>(a.out) + (size_t)t * a.ld_out + n + i * 8 * kPer, x.w[i]);
+    for (int i = 0; i < kWords / 8; ++i) store32(static_cast<O*>(a.out) + (size_t)t * a.ld_out + n + i * 8 * kPer, x.w[i]);
+  }
+  __syncwarp();   // rows past T: the caller's next loads of tensor memory want the warp converged
 }
 
 // Up to 32 rows of up to 32 bytes from `turn` (9 words a row), by a warp.  A call:
@@ -538,6 +541,7 @@ DEV_INLINE void finish_e4m3(const BlockArgs& b, uint32_t d, Column column, int t
   const float inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
   const bool live = t < a.T;
   if (live && n0 < a.N && (kF == 128 || h == 0)) b.qs[(size_t)t * b.nb + n0 / 128] = s;
+  __syncwarp();   // the loads of tensor memory below want the warp converged
   uint8_t* out = static_cast<uint8_t*>(a.out) + (size_t)t * a.ld_out + n0;
 #pragma unroll 1
   for (int c = 0; c < kF && n0 + c < a.N; c += 32) {
@@ -556,6 +560,7 @@ DEV_INLINE void finish_e4m3(const BlockArgs& b, uint32_t d, Column column, int t
     }
     if (b.wide_rows && n0 + c + 32 <= a.N) {
       if (live) store32(out + c, w);
+      __syncwarp();
     } else {
       // other rows are turned, so that the lanes of a store lie side by side, in
       // words or in bytes (T = 2274, N = 5328, K = 112: 18 us, each lane its own

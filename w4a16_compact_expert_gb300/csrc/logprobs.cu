@@ -179,16 +179,20 @@ struct Part {
     return r;
   }
   DEV_INLINE int edge_place(int i) const { return i < head ? i : V - edge + i; }
-  // f(value, place) of every value, in a short loop: for what is rare
+  // f(value, place) of every value: for what is rare
   template <int NT, typename F>
   DEV_INLINE void each(F f) const {
     if ((int)threadIdx.x < edge) {
       const int c = edge_place(threadIdx.x);
       f(blk::to_float(row[c]), c);
     }
-    const int n = windows * Win<E>::N;
+    const uint4* const at = reinterpret_cast<const uint4*>(row + begin);
 #pragma unroll 4
-    for (int c = threadIdx.x; c < n; c += NT) f(blk::to_float(row[begin + c]), begin + c);
+    for (int w = threadIdx.x; w < windows; w += NT) {
+      const uint4 v = at[w];
+#pragma unroll
+      for (int j = 0; j < Win<E>::N; ++j) f(blk::to_float(reinterpret_cast<const E*>(&v)[j]), begin + w * Win<E>::N + j);
+    }
   }
 };
 
@@ -307,8 +311,10 @@ DEV_INLINE int order_candidates(const unsigned long long* list, int n, int k, Sh
 }
 
 // Candidates of a part in which too many values crowd at the threshold or too
-// few are above the floor: at most kCand into sh.cand, the k largest among
-// them, ties to the lower place.  Their number is returned.
+// few are above the floor: at most kCand into sh.cand, the k largest (or all that
+// are not masked) among them, ties to the lower place.  Their number is returned.
+// Reads the part twice where at most kCand values are not masked: 1000 rows of
+// 131072 BF16 that keep 3 tokens, 20 best, take 244 us (all kept 72).
 template <typename E, int NT, typename Sh>
 __device__ __noinline__ int collect_again(const Part<E>& p, int k, Sh& sh) {
   const int tid = threadIdx.x, lane = tid & 31;
@@ -325,12 +331,16 @@ __device__ __noinline__ int collect_again(const Part<E>& p, int k, Sh& sh) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) n[i] = sh.count[i];
   };
-  // the largest and the smallest of the values that are not masked
+  // the values that are not masked: the largest, the smallest, how many
   uint32_t most = 0, least = 0xffffffffu;
+  int n[3] = {};
   p.template each<NT>([&](float x, int) {
     const uint32_t key = order_key(x);
     most = max(most, key);
-    if (key) least = min(least, key);
+    if (key) {
+      least = min(least, key);
+      ++n[0];
+    }
   });
   most = __reduce_max_sync(0xffffffffu, most);
   least = __reduce_min_sync(0xffffffffu, least);
@@ -347,45 +357,55 @@ __device__ __noinline__ int collect_again(const Part<E>& p, int k, Sh& sh) {
   __syncthreads();
   most = sh.key_max;
   least = sh.key_min;
-  // All that lies above `limit` is collected, and of those that equal it the
-  // first, up to k in all.  The smallest, where few lie above it (a mask by the
-  // lowest value, one value everywhere); else the largest number that k keys
-  // reach, found two bits at a time from the first that the keys do not have in
-  // common.
-  uint32_t limit = least;
-  int n[3] = {};
-  p.template each<NT>([&](float x, int) { n[0] += order_key(x) > least; });
   sum(n);
-  if (n[0] > Sh::kCand) {
-    const int same = __clz(most ^ least) & ~1;
-    limit = same == 0 ? 0u : most >> (32 - same) << (32 - same);
-    for (int shift = 30 - same; shift >= 0; shift -= 2) {
-      n[0] = n[1] = n[2] = 0;
-      p.template each<NT>([&](float x, int) {
-        const uint32_t key = order_key(x);
+  // What reaches `limit` is collected, where it fits; else all that lies above
+  // it, and of those that equal it the first, up to k in all.  The smallest, where
+  // few lie above it (few left by the mask, a mask by the lowest value, one value
+  // everywhere); else the largest number that k keys reach, found two bits at a
+  // time from the first that the keys do not have in common, or the first found
+  // that few enough reach.
+  uint32_t limit = least;
+  int reach = n[0];   // keys that reach `limit`; k or more where there are more than kCand
+  if (reach > Sh::kCand) {
+    n[0] = n[1] = n[2] = 0;
+    p.template each<NT>([&](float x, int) { n[0] += order_key(x) > least; });
+    sum(n);
+    if (n[0] > Sh::kCand) {
+      const int same = __clz(most ^ least) & ~1;
+      limit = same == 0 ? 0u : most >> (32 - same) << (32 - same);
+      for (int shift = 30 - same; shift >= 0 && reach > Sh::kCand; shift -= 2) {
+        n[0] = n[1] = n[2] = 0;
+        p.template each<NT>([&](float x, int) {
+          const uint32_t key = order_key(x);
 #pragma unroll
-        for (uint32_t i = 0; i < 3; ++i) n[i] += key >= (limit | (i + 1) << shift);
-      });
-      sum(n);
-      uint32_t step = 0;
+          for (uint32_t i = 0; i < 3; ++i) n[i] += key >= (limit | (i + 1) << shift);
+        });
+        sum(n);
+        uint32_t step = 0;
 #pragma unroll
-      for (uint32_t i = 0; i < 3; ++i)
-        if (n[i] >= k) step = i + 1;
-      limit |= step << shift;
+        for (uint32_t i = 0; i < 3; ++i)
+          if (n[i] >= k) {
+            step = i + 1;
+            reach = n[i];
+          }
+        limit |= step << shift;
+      }
     }
   }
+  const bool fits = reach <= Sh::kCand;
   if (tid == 0) sh.cand_n = 0;
   __syncthreads();
   p.template each<NT>([&](float x, int c) {
     const uint32_t key = order_key(x);
-    if (key > limit) {
+    if (key > limit || (fits && key == limit)) {
       const int i = atomicAdd(&sh.cand_n, 1);
       if (i < Sh::kCand) sh.cand[i] = candidate(key, c);
     }
   });
   __syncthreads();
-  // in the order of the places: the head, the windows, the tail
   int have = min(sh.cand_n, Sh::kCand);
+  if (fits) return have;   // the same for the whole CTA
+  // in the order of the places: the head, the windows, the tail
   const int inner = p.windows * Win<E>::N, all = inner + p.edge;
   for (int c0 = 0; c0 < all && have < k; c0 += NT) {
     const int i = c0 + tid;

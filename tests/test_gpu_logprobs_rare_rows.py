@@ -4,10 +4,12 @@ Values against the float64 oracle with the bounds of test_gpu_logprobs; times ag
 with bounds a few times what re-reading a row two or three times costs, far below what one element at a time does."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
 from tests.test_gpu_logprobs import TYPES, check, rand, tokens_of
+from tests.test_logprobs_windows import rising
 from w4a16_compact_expert_gb300 import block as B
 from w4a16_compact_expert_gb300 import moe_w4a16 as F
 
@@ -79,3 +81,26 @@ def test_few_left_take_a_few_readings(keep):
     x = rand(T, V, torch.bfloat16, 1)
     few = keep_few(40, V, torch.bfloat16, keep, 2).repeat(T // 40, 1)
     assert micros(few, tok, 20) < 8 * micros(x, tok, 20)
+
+
+@pytest.mark.parametrize("T,threads", [(930, 128), (500, 512)])
+@pytest.mark.parametrize("k", [20, 32])
+def test_rows_that_put_too_much_aside(T, threads, k):
+    """Values that rise along the row: more windows than there is room for, few values at the last threshold."""
+    x = torch.from_numpy(np.stack([rising(threads, i) for i in range(3)])).cuda()
+    x = x.repeat(-(-T // 3), 1)[:T]
+    tok = tokens_of(T, x.shape[1], 3)
+    outs = B.token_logprobs(x, tok, k)
+    for at in (slice(0, 4), slice(T - 3, T)):
+        check(x[at], tok[at], k, [o[at] for o in outs])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["fp32", "fp16", "bf16"])
+def test_the_most_alternatives_take_as_long_as_fewer(dtype):
+    """1000 rows of 131072 in no order: read once for 32 alternatives as for 16 (rows read again took 40 times as long)."""
+    T, V = 1000, 131072
+    tok = tokens_of(T, V, 1)
+    x = rand(T, V, dtype, 1)
+    assert micros(x, tok, 32) < 2 * micros(x, tok, 16)
+    pick = torch.tensor([0, 1, 500, 999], device="cuda")
+    check(x[pick], tok[pick], 32, [o[pick] for o in B.token_logprobs(x, tok, 32)])

@@ -13,13 +13,17 @@
 //
 // The k largest: a thread's m is the largest of its values so far, and k values
 // reach the k-th largest of any groups of threads' maxima.  This threshold is
-// found after the 1st, 2nd, 4th, 8th .. batch of values.  The 16 bytes around a
-// value that reaches it are put aside while they are in registers, about
-// k (1 + log2(batches)) of them per row; in the end those that still reach it
+// found after the 1st, 2nd, 4th, 8th .. batch of values, as the k-th largest of
+// 64 groups' maxima: 64 ln(64 / (64 - k)) values reach it where they come in no
+// order, 8 for k = 8 and 44 for k = 32.  The 16 bytes around a value that
+// reaches it are put aside while they are in registers, about as many
+// times 1 + log2(batches) per row; in the end those that still reach it
 // are gone through, and their values ordered by counting.  (Picking the single
 // values out in the reading loop cost it half as many instructions again.)  Rows
-// in which too many or too few are found (ties, masks of the lowest finite
-// value, fewer than k values left by the mask) are read again.
+// in which more are put aside than there is room for (values that rise along the
+// row) are read once more for what reaches the last threshold; rows in which too
+// many or too few are found (ties, masks of the lowest finite value, fewer than k
+// values left by the mask) a few times.
 //
 // What runs once per row is written in short loops: straight code that is new
 // to the SM costs some 15 cycles an instruction, waiting for itself.
@@ -149,8 +153,9 @@ struct Nothing {};
 template <int NT, bool CLUSTER>
 struct Shared {
   // windows that can be put aside, and candidates among their values; few where
-  // many small CTAs share an SM
-  static constexpr int kWin = NT == 32 ? 128 : 256, kCand = NT == 32 ? 256 : 512;
+  // many small CTAs share an SM, whose rows have no more windows.  Rows of 200000
+  // FP32 in no order put 284 aside for k = 32, 347 at most (128 threads).
+  static constexpr int kWin = NT == 32 ? 128 : 512, kCand = NT == 32 ? 256 : 512;
   static_assert(!CLUSTER || 8 * kSend <= kCand, "the received candidates can all be kept");
   uint4 win[kWin];
   unsigned long long win_max[kWin];   // the window's largest value and its place, as a candidate
@@ -315,9 +320,26 @@ DEV_INLINE int order_candidates(const unsigned long long* list, int n, int k, Sh
 // are not masked) among them, ties to the lower place.  Their number is returned.
 // Reads the part twice where at most kCand values are not masked: 1000 rows of
 // 131072 BF16 that keep 3 tokens, 20 best, take 244 us (all kept 72).
+// from: a number that k keys reach, or 0; where no more do than fit, one reading
+// is enough.
 template <typename E, int NT, typename Sh>
-__device__ __noinline__ int collect_again(const Part<E>& p, int k, Sh& sh) {
+__device__ __noinline__ int collect_again(const Part<E>& p, int k, uint32_t from, Sh& sh) {
   const int tid = threadIdx.x, lane = tid & 31;
+  if (from) {
+    if (tid == 0) sh.cand_n = 0;
+    __syncthreads();
+    p.template each<NT>([&](float x, int c) {
+      const uint32_t key = order_key(x);
+      // not counted on once too many reach it (one value everywhere)
+      if (key >= from && *static_cast<volatile int*>(&sh.cand_n) <= Sh::kCand) {
+        const int i = atomicAdd(&sh.cand_n, 1);
+        if (i < Sh::kCand) sh.cand[i] = candidate(key, c);
+      }
+    });
+    __syncthreads();
+    const int have = sh.cand_n;
+    if (have >= k && have <= Sh::kCand) return have;   // the same for the whole CTA
+  }
   auto sum = [&](int (&n)[3]) {   // over the CTA
     __syncthreads();
     if (tid < 3) sh.count[tid] = 0;
@@ -448,7 +470,7 @@ DEV_INLINE void put_aside(const Win<E> (&v)[U], const float (&wm)[U], float thr,
 template <typename E, int NT, typename Sh>
 DEV_INLINE int open_windows(const Part<E>& p, int k, uint32_t thr, float x_edge, Sh& sh) {
   constexpr int N = Win<E>::N;
-  const int tid = threadIdx.x, n = min(sh.win_n, Sh::kWin);
+  const int tid = threadIdx.x, n = sh.win_n;
   if (tid == 0) sh.cand_n = 0;
   if (n > 64) {
     uint32_t key = 0;
@@ -580,11 +602,12 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
   }
   int n = 0;   // the candidates in sh.cand, or, once ordered, in sh.best
   if (TOP && all.m > -INFINITY) {
-    if (!again) {
+    const bool lost = sh.win_n > Sh::kWin;   // windows
+    if (!again && !lost) {
       n = open_windows<E, NT>(p, a.k, top, x_edge, sh);
-      again = sh.win_n > Sh::kWin || n > Sh::kCand || n < a.k;
+      again = n > Sh::kCand || n < a.k;
     }
-    if (again) n = collect_again<E, NT>(p, a.k, sh);
+    if (again || lost) n = collect_again<E, NT>(p, a.k, lost ? top : 0u, sh);
   }
 
   if constexpr (CLUSTER) {

@@ -133,7 +133,14 @@ DEV_INLINE void reduce_row(float& ss, float& mx, bool want_mx, int nt, int tx, f
   }
 }
 
-constexpr int kTops = 160;   // the most windows of a CTA, over 16
+// Places for block maxima in shared memory, ceil(V nt / 16) for each row of a CTA of
+// nt threads and V windows a thread each: a CTA of one row has up to V MT / 16, one
+// of kRowThreads / nt short rows up to kRowThreads ceil(V / 16) (nt = 1).
+constexpr int kTops = 160, kRowThreads = 128;
+template <int V, int MT>
+constexpr bool tops_fit(bool many_rows) {
+  return (V * MT + 15) / 16 <= kTops && (!many_rows || kRowThreads * ((V + 15) / 16) <= kTops);
+}
 
 // The stores of a row: s, n and q of a thread's windows.
 // BLK: every lane of the warp comes here, also those whose row is not `live`.
@@ -273,6 +280,7 @@ DEV_INLINE void load_weights(const NormArgs& a, const int (&c0)[V], float2 (&w)[
 // multiple of 32), blockDim.y rows per CTA, MT threads at most.
 template <typename E, Access A, int V, int MT, bool BLK>
 __global__ void __launch_bounds__(MT) add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
+  static_assert(tops_fit<V, MT>(true), "the block maxima of a CTA's rows fit");
   __shared__ float2 part[32];
   __shared__ float2 top[BLK && A == kPeeled ? kTops : 1];
   const int nt = blockDim.x, tx = threadIdx.x, H = a.H;
@@ -319,6 +327,7 @@ constexpr int kStreamThreads = V == 1 ? 1280 : V == 2 ? 1024 : 640;   // per SM,
 template <typename E, Access A, int V, int MT, bool BLK>
 __global__ void __launch_bounds__(MT, kStreamThreads<V> / MT) add_rmsnorm_stream_kernel(
     const __grid_constant__ NormArgs a, int ahead) {
+  static_assert(tops_fit<V, MT>(false), "the block maxima of a row fit");
   extern __shared__ __align__(16) uint8_t ring_raw[];   // [ahead + 1][V * (1 or 2)][threads] windows
   __shared__ float2 part[2][32];
   __shared__ float2 top[BLK && A == kPeeled ? kTops : 1];   // read before the next row's first barrier, written after it
@@ -407,7 +416,7 @@ int row_threads(int windows, int V) {
 
 template <typename E, Access A, int V, int MT, bool BLK>
 cudaError_t launch_rows(const NormArgs& a, int windows, cudaStream_t st) {
-  const int nt = row_threads(windows, V), rows = nt >= 128 ? 1 : 128 / nt;
+  const int nt = row_threads(windows, V), rows = nt >= kRowThreads ? 1 : kRowThreads / nt;
   const long long grid = (a.T + rows - 1) / rows;
   return launch_pdl(add_rmsnorm_kernel<E, A, V, MT, BLK>, dim3((unsigned)grid), dim3(nt, rows), 0, st, 1, a);
 }

@@ -104,3 +104,25 @@ def test_the_most_alternatives_take_as_long_as_fewer(dtype):
     assert micros(x, tok, 32) < 2 * micros(x, tok, 16)
     pick = torch.tensor([0, 1, 500, 999], device="cuda")
     check(x[pick], tok[pick], 32, [o[pick] for o in B.token_logprobs(x, tok, 32)])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("T,V", [(1, 70001), (5, 2000), (610, 129), (1300, 500)])
+def test_negative_zero_equals_zero(T, V, dtype):
+    """Zeros of either sign where their order decides the ids: the lower index first."""
+    k = 16
+    rows = []
+    x = torch.zeros(T, V, dtype=dtype, device="cuda")
+    x[:, 0] = x[:, 5] = -0.0
+    rows.append(x)
+    x = torch.zeros(T, V, dtype=dtype, device="cuda")
+    x[:, ::2] = -0.0
+    x[:, 1::9] = -1.0
+    rows.append(x.clone())
+    x[:, [3, V // 2, V - 1]] = 2.0
+    rows.append(x)
+    for x in rows:
+        signed = x[0].double() - 1e-300 * torch.signbit(x[0]).double()   # an order in which -0 is less
+        assert not torch.equal(torch.sort(signed, descending=True, stable=True)[1][:k], torch.sort(x[0].double(), descending=True, stable=True)[1][:k])
+        tok = tokens_of(T, V, 1)
+        check(x, tok, k, B.token_logprobs(x, tok, k))

@@ -125,10 +125,12 @@ def add_rmsnorm(x, residual=None, weight=None, *, eps: float = 1e-6, norm: bool 
     and 128 values instead, q_scale [T, ceil(H / 128)], as linear_blocks takes
     them (rows allocated on the 16-byte grid).  out: the same four, to be written (None where not returned); s may
     be x or residual, y may be x."""
-    blocks = quant == "blocks"
-    if not blocks and isinstance(quant, str):
-        raise ValueError("quant must be True, False or 'blocks'")
-    quant = bool(quant)
+    blocks = False
+    if quant is not False and quant is not True:   # the smallest calls are bound by the host
+        blocks = quant == "blocks"
+        if not blocks and isinstance(quant, str):
+            raise ValueError("quant must be True, False or 'blocks'")
+        quant = bool(quant)
     if out is None:
         dt = x.dtype
         y = _empty(x.shape, dt, x, stream) if norm else None

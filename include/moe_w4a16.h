@@ -492,7 +492,9 @@ typedef struct {
  *   residual_out[t] = s, y[t] = n               (each rounded to dtype; NULL to skip)
  *   q_scale[t] = max_h |n| / 448
  *   q[t] = n / q_scale[t] in E4M3, saturating   (q and q_scale: both or neither)
- * The norm is taken of the unrounded sum and q of the unrounded n.  A row
+ * The norm is taken of the unrounded sum and q of the unrounded n.  n and the
+ * quotient are FP32, so a quotient within 2^-17 (relative) of the middle between
+ * two E4M3 values may become either.  A row
  * whose q_scale would fall below 2^-126 gets q_scale = 0 and q = 0.  NaN and
  * infinities propagate within their row.  residual_out may be x or residual
  * and y may be x (the same pointer and stride).  At least one output is
@@ -505,8 +507,8 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_add_rmsnorm(const moe_w4a16_rmsnorm_con
  * (the last block of a row may be shorter): with nb = ceil(H / 128)
  *   q_scale[t][j] = max over block j of |n| / 448     ([T][nb], contiguous)
  *   q[t][h] = n / q_scale[t][h / 128] in E4M3, saturating
- * Both are required; y and residual_out as there.  A block whose q_scale would
- * fall below 2^-126 gets q_scale = 0 and q = 0. */
+ * Both are required; y, residual_out and what is said of the quotient as there.
+ * A block whose q_scale would fall below 2^-126 gets q_scale = 0 and q = 0. */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_add_rmsnorm_blocks(const moe_w4a16_rmsnorm_config* cfg, int64_t T,
                                                             const void* x, const void* residual, const void* weight,
                                                             void* residual_out, void* y, void* q, float* q_scale,
@@ -613,9 +615,13 @@ typedef struct {
  * The last blocks may be shorter.  An E4M3 output has a scale per row and 128
  * values, as x wants it: out_scale[t][j] = max over block j of |o| / 448
  * ([T][nb], contiguous), out[t][n] = o / out_scale[t][n / 128], of the unrounded
- * o; a scale below 2^-126 is 0, and so are its values.  It takes no residual.
+ * o; a scale below 2^-126 is 0, and so are its values.  It takes no residual.  o
+ * carries the rounding of its sum, so that a quotient that lies as near to the
+ * middle between two E4M3 values may become either.
  * A block's products accumulate in FP32 on the tensor cores, blocks are scaled
- * and added in FP32; a call's result does not change from run to run.
+ * and added in FP32; a call's result does not change from run to run.  The product
+ * x_scale w_scale is formed first: where it passes 2^128 the result is not
+ * finite, and below 2^-126 it loses bits.
  * Activations, alignment of x and W, aliases and bounded waits are those of
  * moe_w4a16_linear. */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_linear_blocks(const moe_w4a16_linear_blocks_config* cfg, int64_t T,

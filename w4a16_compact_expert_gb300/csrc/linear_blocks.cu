@@ -14,18 +14,27 @@
 // tile holds 128 features (SWIGLU: 128 gate and 128 up rows in two accumulators),
 // one block of scales of the output.  8 tokens through W [50304][2048] take 18.4 us
 // (5.6 TB/s), one through SWIGLU [11264][2048] 5.9, 8 through [2048][5632] 5.8: the
-// last two lie on the time of a launch and one trip through the pipeline.
+// last two, whose W lies in the L2 there (from memory 7.0 and 6.7), on the time of a
+// launch and one trip through the pipeline.  More tokens send more between the CTAs,
+// four bytes a store: 17 through SWIGLU [11264][2048] 7.4, 48 11.8 (33 to 48 also
+// spill 120 bytes a thread).
 //
 // linear_blocks_wide_kernel (more tokens): as linear_wide_kernel, CTA pairs over
 // tiles of 256 tokens x BN weight rows, but the accumulators (two of 256 columns,
-// four of fewer) go round by chunks instead of tiles.  What bounds it is the adding,
-// not the tensor cores: a chunk's MMAs take 512 cycles at 256 columns, waking up for
-// its accumulator, reading, adding and handing it back 820 (the packed FP32 FMAs
-// alone 270).  At a tile's end the sums go back into the last chunk's accumulator,
-// so that the rest of the epilogue is a loop over columns: out of registers it has to
-// be unrolled, and its instructions no longer fit the cache.  2048 tokens through
-// SWIGLU [11264][2048] to E4M3 take 51 us (1.9 PFLOP/s), 4096 through [2048][5632]
-// to FP16 47 (2.0 PFLOP/s), a residual added 54.
+// four of fewer) go round by chunks instead of tiles.  A chunk's MMAs take 512
+// cycles at 256 columns, but a chunk takes 820: waking up for its accumulator,
+// reading, adding (the packed FP32 FMAs 270) and handing it back, one after the
+// other in each warp.  The warps that add also finish the tile, and no chunk is added
+// meanwhile (3.0 of a tile's 9.7 us at K = 2048 by the rule of wide_rows).  At a
+// tile's end the sums go back into the last chunk's accumulator, so that the rest of
+// the epilogue is a loop over columns: out of registers it has to be unrolled, and
+// its instructions no longer fit the cache.  2048 tokens through SWIGLU [11264][2048]
+// to E4M3 take 51 us (1.84 PFLOP/s), 4096 through [2048][5632] to FP16 47 (2.0
+// PFLOP/s), a residual added 54.  Furthest from their bytes and operations are 65 to
+// 256 tokens (tiles hold 256, K is not split: SWIGLU [11264][2048] 12.3 to 12.8 us,
+// [2048][5632] 11.6) and short K, where the end of a tile is most of it (4096 tokens,
+// [32768][512] to FP16 154 us).  At 128 and 256 rows up to 32 bytes of a thread's sums
+// and addresses are spilled.
 #include "linear_dev.cuh"
 
 namespace {
@@ -76,9 +85,12 @@ DEV_INLINE float2 pair_at(const uint32_t (&r)[N], int j) {
   return make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
 }
 
-// Arrives at a cluster address.  Nothing but tensor memory changes hands, whose
-// reads tcgen05.fence::before_thread_sync has ordered: a release at cluster scope
-// waits for the thread's memory accesses, 1,200 cycles a chunk here.
+// Arrives at a cluster address, by one lane for its warp.  Nothing but tensor
+// memory changes hands: every lane's reads of it have returned (wait::ld) before the
+// __syncwarp in front of the arrival, so nothing that follows can overwrite what
+// is still to be read, and tcgen05.fence::before_thread_sync orders them before it.
+// A release at cluster scope waits for the thread's other memory accesses too:
+// 2048 tokens through SWIGLU [11264][2048] 93 us instead of 53.
 DEV_INLINE void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

@@ -4,8 +4,9 @@
 //   entropy = ln S - sum e^(x - M) (x - M) / S.
 //
 // Bound by reading the logits once: 4096 rows of 131072 BF16 take 165 us (6.5
-// TB/s), with 8 alternatives 208; 64 of 151936 FP32 with 5 alternatives 13.2, one
-// of 50304 with 20 5.2, of which the reading is 3.0 and finding them the rest.  A row is read by one CTA, or, where there
+// TB/s), with 8 alternatives 208, with 32 232; 64 of 151936 FP32 with 5 alternatives
+// 13.2, one of 50304 with 20 5.2, of which the reading is 3.0 and finding them the
+// rest.  A row is read by one CTA, or, where there
 // are few rows, by the CTAs of a cluster; every thread keeps the running
 // maximum m of its values and the two sums relative to it, which are rescaled
 // once per batch of values; threads and CTAs join by rescaling to the common

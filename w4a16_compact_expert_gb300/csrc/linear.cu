@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(192, 2)
       if (GATED) prefetch_box(&tmW, (rank + i * S) * kElem, a.N + n0, leader);
     }
   }
+  __syncwarp();   // tensor memory wants the warp converged
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::kCols);
     tmem_relinquish();
@@ -307,6 +308,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     mbar_init(last, 1);
     fence_mbar_init();
   }
+  __syncwarp();
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(kCols)

@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(192, PER)
       if (GATED) prefetch_box(&tmW, (rank + i * S) * 128, a.N + n0, leader);
     }
   }
+  __syncwarp();   // tensor memory and cluster barriers want the warp converged, here and below
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::kCols);
     tmem_relinquish();
@@ -315,6 +316,7 @@ __global__ void __launch_bounds__(192, PER)
 
   // Token c of the tile belongs to rank c % S: every CTA sends its part of c's
   // rows there, as slot c / S, and the owner adds the parts in rank order.
+  __syncwarp();
   if (S > 1) {
     if (!C::kOwnRecv) cluster_arrive();   // this CTA's stages are free
     cluster_wait();
@@ -635,6 +637,7 @@ __global__ void __launch_bounds__(WideCfg<BN>::kThreads, 1)
     mbar_init(last, 1);
     fence_mbar_init();
   }
+  __syncwarp();
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(kCols)

@@ -533,7 +533,10 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
   if (TOP && tid == 0) sh.win_n = 0;   // before the first batch's barrier
   pdl_wait();
   pdl_trigger();
-  if (CLUSTER) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if constexpr (CLUSTER) {
+    __syncwarp();   // cluster barriers want the warp converged
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
 
   const float floor = floor_of<E>();
   Win<E> next[U];
@@ -617,6 +620,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
       n = order_here<NT>(n, a.k, sh);
       list = sh.best;
     }
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // the first CTA runs
     if (TOP && tid < kSend)   // turned by 8 per CTA, so that they spread over order_candidates' groups
       st_cluster_u64(map_to_rank(&sh.from.cand[rank * kSend + (tid + 8 * rank) % kSend], 0), tid < n ? list[tid] : 0);
@@ -626,6 +630,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
       st_cluster_f32(at + 4, all.s);
       st_cluster_f32(at + 8, all.e);
     }
+    __syncwarp();
     cluster_sync();
     if (rank != 0) return;
     all = warp_join(lane < S ? sh.from.stat[lane] : Stat{-INFINITY, 0.f, 0.f});

@@ -12,11 +12,11 @@
 // once): as linear_narrow_kernel, W as the 128-row operand, the K chunks of a tile
 // dealt to the CTAs of a cluster, parts added by a token's owner in rank order.  A
 // tile holds 128 features (SWIGLU: 128 gate and 128 up rows in two accumulators),
-// one block of scales of the output.  8 tokens through W [50304][2048] take 18.4 us
-// (5.6 TB/s), one through SWIGLU [11264][2048] 5.9, 8 through [2048][5632] 5.8: the
-// last two, whose W lies in the L2 there (from memory 7.0 and 6.7), on the time of a
+// one block of scales of the output.  8 tokens through W [50304][2048] take 18.2 us
+// (5.6 TB/s), one through SWIGLU [11264][2048] 5.8, 8 through [2048][5632] 5.7: the
+// last two, whose W lies in the L2 there (from memory about 7), on the time of a
 // launch and one trip through the pipeline.  More tokens send more between the CTAs,
-// four bytes a store: 17 through SWIGLU [11264][2048] 7.4, 48 11.8 (33 to 48 also
+// four bytes a store: 17 through SWIGLU [11264][2048] 7.2, 48 11.9 (33 to 48 also
 // spill 120 bytes a thread).
 //
 // linear_blocks_wide_kernel (more tokens): as linear_wide_kernel, CTA pairs over
@@ -29,11 +29,11 @@
 // tile's end the sums go back into the last chunk's accumulator, so that the rest of
 // the epilogue is a loop over columns: out of registers it has to be unrolled, and
 // its instructions no longer fit the cache.  2048 tokens through SWIGLU [11264][2048]
-// to E4M3 take 51 us (1.84 PFLOP/s), 4096 through [2048][5632] to FP16 47 (2.0
-// PFLOP/s), a residual added 54.  Furthest from their bytes and operations are 65 to
-// 256 tokens (tiles hold 256, K is not split: SWIGLU [11264][2048] 12.3 to 12.8 us,
+// to E4M3 take 51 us (1.84 PFLOP/s), 4096 through [2048][5632] to FP16 46 (2.0
+// PFLOP/s), a residual added 52.  Furthest from their bytes and operations are 65 to
+// 256 tokens (tiles hold 256, K is not split: SWIGLU [11264][2048] 12.5 to 13.1 us,
 // [2048][5632] 11.6) and short K, where the end of a tile is most of it (4096 tokens,
-// [32768][512] to FP16 154 us).  At 128 and 256 rows up to 32 bytes of a thread's sums
+// [32768][512] to FP16 150 us).  At 128 and 256 rows up to 32 bytes of a thread's sums
 // and addresses are spilled.
 #include "linear_dev.cuh"
 
